@@ -7,6 +7,7 @@
 // rather than fall back; hipfire, "Implementation requirements for
 // multi-weight Q8 WMMA dispatch": check dtypes and that K is a whole number
 // of blocks so no kernel silently drops a tail).
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -105,6 +106,99 @@ static int32_t check_weights(const qmv_weights* W) {
 using qmv::fail;
 
 namespace qmv {
+
+static bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+static int32_t check_workspace(const void* ws, uint64_t bytes, uint64_t need, const char* asks) {
+  if (!ws && need) return fail(QMV_ERR_NULL, "workspace is NULL (%s)", asks);
+  if (!aligned_to(ws, 256)) return fail(QMV_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (bytes < need)
+    return fail(QMV_ERR_SIZE, "workspace holds %llu bytes, this call needs %llu (%s)", (unsigned long long)bytes,
+                (unsigned long long)need, asks);
+  return QMV_OK;
+}
+
+// Everything of the arguments that is on the host.  (Strides are bounded so
+// that no offset computed from them in 64 bits can wrap.)
+static int32_t check_attn(const qmv_attn_args* a) {
+  if (!a) return fail(QMV_ERR_NULL, "arguments are NULL");
+  if (a->dtype != QMV_F16 && a->dtype != QMV_BF16) return fail(QMV_ERR_UNSUPPORTED, "dtype %d", a->dtype);
+  if (a->head_dim < 8 || a->head_dim > 256 || a->head_dim % 8)
+    return fail(QMV_ERR_UNSUPPORTED, "head_dim %d (a multiple of 8 up to 256)", a->head_dim);
+  if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
+    return fail(QMV_ERR_SHAPE, "heads %d, kv_heads %d", a->heads, a->kv_heads);
+  if (a->rows < 0 || a->nseq < 0 || a->prefix_len < 0 || a->max_suffix < 0 || a->num_pages < 0)
+    return fail(QMV_ERR_SHAPE, "rows %lld, nseq %d, prefix_len %lld, max_suffix %lld or num_pages %lld < 0",
+                (long long)a->rows, a->nseq, (long long)a->prefix_len, (long long)a->max_suffix,
+                (long long)a->num_pages);
+  if (!(a->scale > 0.f) || isinf(a->scale)) return fail(QMV_ERR_RANGE, "scale %g is not positive and finite", a->scale);
+  if (a->rows == 0) return QMV_OK;
+  if (a->nseq < 1 || a->max_rows < 1) return fail(QMV_ERR_SHAPE, "nseq %d or max_rows %d < 1", a->nseq, a->max_rows);
+  if (a->rows > (int64_t{1} << 20) || a->rows * a->heads > (int64_t{1} << 24) || a->prefix_len > INT32_MAX / 2 ||
+      a->max_suffix > INT32_MAX / 2 || a->num_pages > INT32_MAX || a->nseq > (1 << 20))
+    return fail(QMV_ERR_UNSUPPORTED, "rows %lld (x %d heads), nseq %d, prefix_len %lld, max_suffix %lld or "
+                "num_pages %lld too large", (long long)a->rows, a->heads, a->nseq, (long long)a->prefix_len,
+                (long long)a->max_suffix, (long long)a->num_pages);
+  if (a->tree_mask && a->max_rows > 64)
+    return fail(QMV_ERR_UNSUPPORTED, "tree_mask with max_rows %d above 64", a->max_rows);
+  const bool paged = a->max_suffix > 0 || (a->prefix_len > 0 && a->prefix_pages);
+  if (paged && (a->page_size < 1 || a->page_size > 65536 || (a->page_size & (a->page_size - 1))))
+    return fail(QMV_ERR_SHAPE, "page_size %d is no power of two up to 65536", a->page_size);
+  if (!a->q || !a->out || !a->row_start) return fail(QMV_ERR_NULL, "q, out or row_start is NULL");
+  if (a->prefix_len > 0 && !a->prefix_pages && (!a->k_prefix || !a->v_prefix))
+    return fail(QMV_ERR_NULL, "k_prefix or v_prefix is NULL");
+  if (paged && a->num_pages > 0 && (!a->k_pages || !a->v_pages))
+    return fail(QMV_ERR_NULL, "k_pages or v_pages is NULL");
+  if (a->max_suffix > 0 && (!a->block_table || !a->suffix_len))
+    return fail(QMV_ERR_NULL, "block_table or suffix_len is NULL");
+  if (a->max_suffix > 0 && a->table_stride < (a->max_suffix + a->page_size - 1) / a->page_size)
+    return fail(QMV_ERR_SIZE, "table_stride %lld holds fewer than max_suffix %lld tokens", (long long)a->table_stride,
+                (long long)a->max_suffix);
+  for (const int64_t st : {a->q_row, a->q_head, a->out_row, a->out_head, a->prefix_row, a->prefix_head,
+                           a->page_stride, a->page_row, a->page_head})
+    if (st < 0 || st > (int64_t{1} << 31) || st % 8)
+      return fail(QMV_ERR_SHAPE, "stride %lld (a multiple of 8 up to 2^31)", (long long)st);
+  if (a->table_stride < 0 || a->table_stride > INT32_MAX)
+    return fail(QMV_ERR_SHAPE, "table_stride %lld", (long long)a->table_stride);
+  for (const void* p : {a->q, a->k_prefix, a->v_prefix, a->k_pages, a->v_pages, static_cast<const void*>(a->out)})
+    if (!aligned16(p)) return fail(QMV_ERR_ALIGN, "q, k, v or out not 16-byte aligned");
+  for (const void* p : {static_cast<const void*>(a->prefix_pages), static_cast<const void*>(a->block_table),
+                        static_cast<const void*>(a->row_start), static_cast<const void*>(a->suffix_len),
+                        static_cast<const void*>(a->lse)})
+    if (!aligned_to(p, 4)) return fail(QMV_ERR_ALIGN, "an int32 or fp32 pointer is not 4-byte aligned");
+  if (!aligned_to(a->tree_mask, 8)) return fail(QMV_ERR_ALIGN, "tree_mask not 8-byte aligned");
+  return QMV_OK;
+}
+
+static int32_t check_verify(const qmv_verify_args* a) {
+  if (!a) return fail(QMV_ERR_NULL, "arguments are NULL");
+  if (a->logits_dtype != QMV_F32 && a->logits_dtype != QMV_F16 && a->logits_dtype != QMV_BF16)
+    return fail(QMV_ERR_UNSUPPORTED, "logits dtype %d", a->logits_dtype);
+  if (a->rows < 0 || a->nseq < 0 || a->vocab < 1)
+    return fail(QMV_ERR_SHAPE, "rows %lld or nseq %d < 0, or vocab %lld < 1", (long long)a->rows, a->nseq,
+                (long long)a->vocab);
+  if (a->nseq == 0 && a->rows > 0) return fail(QMV_ERR_SHAPE, "rows %lld of no sequence", (long long)a->rows);
+  if (a->nseq == 0) return QMV_OK;
+  if (a->max_rows < 1) return fail(QMV_ERR_SHAPE, "max_rows %d < 1", a->max_rows);
+  if (a->vocab > (1 << 24) || a->rows > 65535 || a->nseq > 65535)
+    return fail(QMV_ERR_UNSUPPORTED, "vocab %lld above 2^24, or rows %lld or nseq %d above 65535",
+                (long long)a->vocab, (long long)a->rows, a->nseq);
+  if (!a->row_start || !a->accepted || !a->u_sample) return fail(QMV_ERR_NULL, "row_start, u_sample or accepted is NULL");
+  if (a->rows && (!a->logits || !a->tokens || !a->u_accept || !a->out_tokens))
+    return fail(QMV_ERR_NULL, "logits, tokens, u_accept or out_tokens is NULL");
+  if (a->logits_row < a->vocab || a->logits_row > (int64_t{1} << 31) ||
+      (a->draft_probs && (a->draft_row < a->vocab || a->draft_row > (int64_t{1} << 31))))
+    return fail(QMV_ERR_SHAPE, "logits_row %lld or draft_row %lld below vocab %lld or above 2^31",
+                (long long)a->logits_row, (long long)a->draft_row, (long long)a->vocab);
+  if (!aligned_to(a->logits, a->logits_dtype == QMV_F32 ? 4 : 2))
+    return fail(QMV_ERR_ALIGN, "logits not aligned to their type");
+  for (const void* p : {static_cast<const void*>(a->draft_probs), static_cast<const void*>(a->tokens),
+                        static_cast<const void*>(a->row_start), static_cast<const void*>(a->temperature),
+                        static_cast<const void*>(a->u_accept), static_cast<const void*>(a->u_sample),
+                        static_cast<const void*>(a->out_tokens), static_cast<const void*>(a->accepted)})
+    if (!aligned_to(p, 4)) return fail(QMV_ERR_ALIGN, "a pointer is not 4-byte aligned");
+  return QMV_OK;
+}
 
 // A paired launch of two matrices of one format, layout and shape (`a` with
 // twice its rows; launch.h): both outputs, or with glu the SwiGLU input.
@@ -539,6 +633,58 @@ int32_t qmv_dequant(const qmv_weights* W, void* out, int32_t out_dtype, void* st
   if (!qmv::aligned16(out)) return fail(QMV_ERR_ALIGN, "output not 16-byte aligned");
   return qmv::from_hip(qmv::dequant(*W, out, out_dtype, static_cast<hipStream_t>(stream)),
                        "qmv_dequant launch");
+}
+
+int32_t qmv_embed(const qmv_weights* W, const int32_t* ids, int64_t n, float scale, void* out, int32_t out_dtype,
+                  void* stream) {
+  const int32_t st = qmv::check_weights(W);
+  if (st != QMV_OK) return st;
+  if (n < 0) return fail(QMV_ERR_SHAPE, "n %lld < 0", (long long)n);
+  if (out_dtype != QMV_F32 && out_dtype != QMV_F16 && out_dtype != QMV_BF16)
+    return fail(QMV_ERR_UNSUPPORTED, "output dtype %d", out_dtype);
+  if (n == 0) return qmv::ok();
+  if (!ids || !out) return fail(QMV_ERR_NULL, "ids or out is NULL");
+  if (!qmv::aligned16(out) || !qmv::aligned_to(ids, 4))
+    return fail(QMV_ERR_ALIGN, "out not 16-byte or ids not 4-byte aligned");
+  if (n > INT32_MAX || n > (int64_t{1} << 40) / W->cols) return fail(QMV_ERR_UNSUPPORTED, "output too large");
+  return qmv::from_hip(qmv::embed(*W, ids, n, scale, out, out_dtype, static_cast<hipStream_t>(stream)),
+                       "qmv_embed launch");
+}
+
+int32_t qmv_attn_workspace_size(const qmv_attn_args* a, uint64_t* bytes) {
+  if (!bytes) return fail(QMV_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  const int32_t st = qmv::check_attn(a);
+  if (st != QMV_OK) return st;
+  if (a->rows) *bytes = qmv::attn_workspace(*a);
+  return qmv::ok();
+}
+
+int32_t qmv_attn(const qmv_attn_args* a, void* workspace, uint64_t workspace_bytes, void* stream) {
+  int32_t st = qmv::check_attn(a);
+  if (st != QMV_OK) return st;
+  if (a->rows == 0) return qmv::ok();
+  st = qmv::check_workspace(workspace, workspace_bytes, qmv::attn_workspace(*a), "qmv_attn_workspace_size");
+  if (st != QMV_OK) return st;
+  return qmv::from_hip(qmv::attn(*a, workspace, static_cast<hipStream_t>(stream)), "qmv_attn launch");
+}
+
+int32_t qmv_verify_workspace_size(const qmv_verify_args* a, uint64_t* bytes) {
+  if (!bytes) return fail(QMV_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  const int32_t st = qmv::check_verify(a);
+  if (st != QMV_OK) return st;
+  if (a->nseq) *bytes = qmv::verify_workspace(*a);
+  return qmv::ok();
+}
+
+int32_t qmv_verify(const qmv_verify_args* a, void* workspace, uint64_t workspace_bytes, void* stream) {
+  int32_t st = qmv::check_verify(a);
+  if (st != QMV_OK) return st;
+  if (a->nseq == 0) return qmv::ok();
+  st = qmv::check_workspace(workspace, workspace_bytes, qmv::verify_workspace(*a), "qmv_verify_workspace_size");
+  if (st != QMV_OK) return st;
+  return qmv::from_hip(qmv::verify(*a, workspace, static_cast<hipStream_t>(stream)), "qmv_verify launch");
 }
 
 int64_t qmv_probe_read_outputs(uint64_t nbytes) { return qmv::probe_read_blocks(nbytes); }

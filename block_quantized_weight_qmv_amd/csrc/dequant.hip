@@ -186,6 +186,29 @@ __device__ __forceinline__ uint32_t f32_to_f16_rne(float f) {
   return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
 }
 
+// Weights k .. k + 3 of row r.
+template <int FMT>
+__device__ __forceinline__ void dq_quad(const uint8_t* w, uint64_t scales_offset, int cols, int r, int k, float* v) {
+  if (FMT == QMV_Q8_0) {
+    dq_q8_0(w + static_cast<size_t>(r) * (cols / 32) * 34, k, v);
+  } else if (FMT == QMV_Q4_K) {
+    dq_q4_k(w + static_cast<size_t>(r) * (cols / 256) * 144, k, v);
+  } else if (FMT == kQ4KPlanes) {
+    dq_q4_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
+  } else if (FMT == kQ5KPlanes) {
+    dq_q5_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
+  } else if (FMT == kQ6KPlanes) {
+    dq_q6_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
+  } else if (FMT == QMV_Q5_K) {
+    dq_q5_k(w + static_cast<size_t>(r) * (cols / 256) * 176, k, v);
+  } else if (FMT == QMV_Q6_K) {
+    dq_q6_k(w + static_cast<size_t>(r) * (cols / 256) * 210, k, v);
+  } else {
+    dq_int4(w + static_cast<size_t>(r) * (cols / 2), w + scales_offset + static_cast<size_t>(r) * (cols / 128) * 2, k,
+            v);
+  }
+}
+
 template <int FMT, int OUT>
 __global__ void __launch_bounds__(256)
 dequant_kernel(const uint8_t* __restrict__ w, uint64_t scales_offset, int rows, int cols,
@@ -197,24 +220,7 @@ dequant_kernel(const uint8_t* __restrict__ w, uint64_t scales_offset, int rows, 
     const int r = static_cast<int>(idx / quads_per_row);
     const int k = static_cast<int>(idx % quads_per_row) * 4;
     float v[4];
-    if (FMT == QMV_Q8_0) {
-      dq_q8_0(w + static_cast<size_t>(r) * (cols / 32) * 34, k, v);
-    } else if (FMT == QMV_Q4_K) {
-      dq_q4_k(w + static_cast<size_t>(r) * (cols / 256) * 144, k, v);
-    } else if (FMT == kQ4KPlanes) {
-      dq_q4_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
-    } else if (FMT == kQ5KPlanes) {
-      dq_q5_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
-    } else if (FMT == kQ6KPlanes) {
-      dq_q6_k_planes(w, scales_offset, static_cast<int64_t>(r) * (cols / 256) + k / 256, k, v);
-    } else if (FMT == QMV_Q5_K) {
-      dq_q5_k(w + static_cast<size_t>(r) * (cols / 256) * 176, k, v);
-    } else if (FMT == QMV_Q6_K) {
-      dq_q6_k(w + static_cast<size_t>(r) * (cols / 256) * 210, k, v);
-    } else {
-      dq_int4(w + static_cast<size_t>(r) * (cols / 2),
-              w + scales_offset + static_cast<size_t>(r) * (cols / 128) * 2, k, v);
-    }
+    dq_quad<FMT>(w, scales_offset, cols, r, k, v);
     const size_t o = static_cast<size_t>(r) * cols + k;
     if (OUT == QMV_F32) {
       *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
@@ -267,6 +273,79 @@ hipError_t dequant(const qmv_weights& W, void* out, int out_dtype, hipStream_t s
     case QMV_Q5_K: return dequant_fmt<QMV_Q5_K>(W, out, out_dtype, s);
     case QMV_Q6_K: return dequant_fmt<QMV_Q6_K>(W, out, out_dtype, s);
     case QMV_INT4_G128: return dequant_fmt<QMV_INT4_G128>(W, out, out_dtype, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// out[i] = scale * W[ids[i]]: one workgroup per looked-up row (grid y) and
+// 1024 columns (grid x).
+template <int FMT, int OUT>
+__global__ void __launch_bounds__(256)
+embed_kernel(const uint8_t* __restrict__ w, uint64_t scales_offset, int rows, int cols, const int32_t* __restrict__ ids,
+             int64_t n, float scale, void* __restrict__ out) {
+  const int quads = cols / 4;
+  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; idx < n * quads;
+       idx += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t i = idx / quads;
+    const int k = static_cast<int>(idx % quads) * 4;
+    const int r = ids[i];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r >= 0 && r < rows) dq_quad<FMT>(w, scales_offset, cols, r, k, v);
+    const size_t o = static_cast<size_t>(i) * cols + k;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= scale;
+    if (OUT == QMV_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = OUT == QMV_F16 ? f32_to_f16_rne(v[e]) : f32_to_bf16_rne(v[e]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) =
+          make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    }
+  }
+}
+
+template <int FMT>
+static hipError_t embed_fmt(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
+                            hipStream_t s) {
+  const int rows = static_cast<int>(W.rows), cols = static_cast<int>(W.cols);
+  const int64_t want = (n * (cols / 4) + 255) / 256;
+  const int grid = static_cast<int>(want < 65536 ? want : 65536);
+  const uint8_t* w = static_cast<const uint8_t*>(W.data);
+  switch (out_dtype) {
+    case QMV_F32:
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F32>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
+                         ids, n, scale, out);
+      break;
+    case QMV_F16:
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F16>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
+                         ids, n, scale, out);
+      break;
+    case QMV_BF16:
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_BF16>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
+                         ids, n, scale, out);
+      break;
+    default:
+      return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t embed(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
+                 hipStream_t s) {
+  if (W.layout == QMV_LAYOUT_PLANES) {
+    if (W.fmt == QMV_Q4_K) return embed_fmt<kQ4KPlanes>(W, ids, n, scale, out, out_dtype, s);
+    if (W.fmt == QMV_Q5_K) return embed_fmt<kQ5KPlanes>(W, ids, n, scale, out, out_dtype, s);
+    if (W.fmt == QMV_Q6_K) return embed_fmt<kQ6KPlanes>(W, ids, n, scale, out, out_dtype, s);
+    return hipErrorInvalidValue;
+  }
+  switch (W.fmt) {
+    case QMV_Q8_0: return embed_fmt<QMV_Q8_0>(W, ids, n, scale, out, out_dtype, s);
+    case QMV_Q4_K: return embed_fmt<QMV_Q4_K>(W, ids, n, scale, out, out_dtype, s);
+    case QMV_Q5_K: return embed_fmt<QMV_Q5_K>(W, ids, n, scale, out, out_dtype, s);
+    case QMV_Q6_K: return embed_fmt<QMV_Q6_K>(W, ids, n, scale, out, out_dtype, s);
+    case QMV_INT4_G128: return embed_fmt<QMV_INT4_G128>(W, ids, n, scale, out, out_dtype, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -160,6 +160,16 @@ hipError_t gemm_q4_k_f16(const qmv_weights& W, const void* x, float* y, int64_t 
                          hipStream_t s);
 
 hipError_t dequant(const qmv_weights& W, void* out, int out_dtype, hipStream_t s);
+// Rows ids[0 .. n) of W times scale (dequant.hip).
+hipError_t embed(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
+                 hipStream_t s);
+
+// Attention over a shared prefix and paged suffixes (attn.hip) and the
+// verification of drafted tokens (verify.hip), after validation.
+size_t attn_workspace(const qmv_attn_args& a);
+hipError_t attn(const qmv_attn_args& a, void* ws, hipStream_t s);
+size_t verify_workspace(const qmv_verify_args& a);
+hipError_t verify(const qmv_verify_args& a, void* ws, hipStream_t s);
 
 // Canonical Q4_K / Q5_K / Q6_K blocks -> plane layout (planes.h) at dst.
 hipError_t repack_q4_k_planes(const qmv_weights& src, void* dst, hipStream_t s);

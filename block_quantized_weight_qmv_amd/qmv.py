@@ -49,6 +49,26 @@ class QmvGemvItem(ctypes.Structure):
     _fields_ = [("W", ctypes.POINTER(QmvWeights)), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
+class QmvAttnArgs(ctypes.Structure):
+    """Mirror of struct qmv_attn_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "head_dim", "heads", "kv_heads", "nseq", "max_rows",
+                                              "page_size")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "prefix_len", "max_suffix", "num_pages", "table_stride",
+                                              "q_row", "q_head", "out_row", "out_head", "prefix_row", "prefix_head",
+                                              "page_stride", "page_row", "page_head")] + \
+               [(n, ctypes.c_void_p) for n in ("q", "k_prefix", "v_prefix", "prefix_pages", "k_pages", "v_pages",
+                                               "block_table", "row_start", "suffix_len", "tree_mask", "out", "lse")]
+
+
+class QmvVerifyArgs(ctypes.Structure):
+    """Mirror of struct qmv_verify_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("logits_dtype", "nseq", "max_rows", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("rows", "vocab", "logits_row", "draft_row")] + \
+               [(n, ctypes.c_void_p) for n in ("logits", "draft_probs", "tokens", "row_start", "temperature",
+                                               "u_accept", "u_sample", "out_tokens", "accepted")]
+
+
 _lib = None
 
 _i32, _i64, _u64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
@@ -73,6 +93,11 @@ _SIGS = {
     "qmv_gemv_swiglu": (_i32, [_i32, ctypes.POINTER(QmvWeights), ctypes.POINTER(QmvWeights), _p, _i32, _p,
                                _i64, _i64, _i64, _p]),
     "qmv_dequant": (_i32, [ctypes.POINTER(QmvWeights), _p, _i32, _p]),
+    "qmv_embed": (_i32, [ctypes.POINTER(QmvWeights), _p, _i64, ctypes.c_float, _p, _i32, _p]),
+    "qmv_attn_workspace_size": (_i32, [ctypes.POINTER(QmvAttnArgs), ctypes.POINTER(_u64)]),
+    "qmv_attn": (_i32, [ctypes.POINTER(QmvAttnArgs), _p, _u64, _p]),
+    "qmv_verify_workspace_size": (_i32, [ctypes.POINTER(QmvVerifyArgs), ctypes.POINTER(_u64)]),
+    "qmv_verify": (_i32, [ctypes.POINTER(QmvVerifyArgs), _p, _u64, _p]),
     "qmv_probe_read_outputs": (_i64, [_u64]),
     "qmv_probe_read": (_i32, [_p, _u64, _p, _p]),
     "qmv_probe_copy": (_i32, [_p, _p, _u64, _p]),
@@ -365,6 +390,209 @@ def qmv_dequant(W: QmvWeights, out, out_dtype, stream=None) -> None:
     od = _dtype(out_dtype)
     _check_dev(out, "out", od, W.rows * W.cols)
     _check(lib().qmv_dequant(ctypes.byref(W), _ptr(out), _dtype(out_dtype), _stream(stream, out)))
+
+
+# Element types of the index, mask and number tensors of the step's operators.
+_I32, _I64, _F32 = ("int32",), ("int64", "uint64"), ("float32",)
+
+
+def _check_vec(t, what: str, names, n: int) -> None:
+    """A contiguous device tensor of one of the named element types with at least n elements."""
+    if t is None:
+        raise QmvError(-1, f"{what} is None")
+    _check_dev(t, what, None, 0)
+    if isinstance(t, int):
+        return
+    name = str(t.dtype).replace("torch.", "")
+    if name not in names:
+        raise QmvError(-2, f"{what}: tensor dtype {name}, expected one of {names}")
+    if t.numel() < n:
+        raise QmvError(-5, f"{what}: holds {t.numel()} elements, needs {n}")
+
+
+def _check_view(t, what: str, name: str, ndim: int) -> None:
+    """A device tensor of any strides whose last dimension is contiguous."""
+    if t is None:
+        raise QmvError(-1, f"{what} is None")
+    if not getattr(t, "is_cuda", False):
+        raise QmvError(-6, f"{what}: tensor is not on a GPU")
+    if str(t.dtype).replace("torch.", "") != name:
+        raise QmvError(-2, f"{what}: tensor dtype {t.dtype}, expected {name}")
+    if t.dim() != ndim:
+        raise QmvError(-3, f"{what}: {t.dim()} dimensions, expected {ndim}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise QmvError(-6, f"{what}: the last dimension is not contiguous")
+
+
+def _strides(t) -> list:
+    """Strides with zero for dimensions of one element, whose stride says nothing."""
+    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(t.dim() - 1)]
+
+
+def _check_one_device(pairs) -> None:
+    devices = {str(t.device) for _, t in pairs if t is not None and hasattr(t, "device")}
+    if len(devices) > 1:
+        raise QmvError(-6, f"{', '.join(n for n, t in pairs if t is not None)}: tensors on {sorted(devices)}")
+
+
+def qmv_embed(W: QmvWeights, ids, n: int, out, out_dtype, scale: float = 1.0, stream=None) -> None:
+    """out[i] = scale * W[ids[i]] for n int32 device ids; ids outside the table give rows of zeros."""
+    od = _dtype(out_dtype)
+    if n > 0:
+        _check_vec(ids, "ids", _I32, n)
+        _check_dev(out, "out", od, n * W.cols)
+    _check(lib().qmv_embed(ctypes.byref(W), _ptr(ids), n, scale, _ptr(out), od, _stream(stream, out)))
+
+
+def qmv_create_attn(q, out, row_start, max_rows: int, *, scale: float, k_prefix=None, v_prefix=None,
+                    prefix_pages=None, prefix_len: int | None = None, k_pages=None, v_pages=None, block_table=None,
+                    suffix_len=None, max_suffix: int = 0, tree_mask=None, lse=None) -> QmvAttnArgs:
+    """Checked arguments of qmv_attn from device tensors, kept alive with them.
+
+    q, out [rows, heads, D]; the prefix as k_prefix, v_prefix [tokens, kv_heads, D], or as prefix_pages (int32 page
+    numbers) with prefix_len; k_pages, v_pages [pages, page_size, kv_heads, D]; block_table [nseq, entries] int32;
+    row_start [nseq + 1], suffix_len [nseq] int32; tree_mask [rows] int64 bits; lse [rows, heads] float32.  Any
+    strides with contiguous last dimensions (k and v of a pair alike)."""
+    a = QmvAttnArgs()
+    if getattr(q, "dtype", None) is None or str(q.dtype) not in ("torch.float16", "torch.bfloat16"):
+        raise QmvError(-6, f"q: {getattr(q, 'dtype', type(q))}, expected a float16 or bfloat16 tensor")
+    name = str(q.dtype).replace("torch.", "")
+    _check_view(q, "q", name, 3)
+    _check_view(out, "out", name, 3)
+    rows, heads, d = (int(x) for x in q.shape)
+    if tuple(out.shape) != (rows, heads, d):
+        raise QmvError(-3, f"out: shape {tuple(out.shape)}, expected {(rows, heads, d)}")
+    _check_vec(row_start, "row_start", _I32, 1)
+    nseq = int(row_start.numel()) - 1
+    a.dtype, a.rows, a.heads, a.head_dim = _dtype(q.dtype), rows, heads, d
+    a.nseq, a.max_rows, a.max_suffix, a.scale = nseq, max_rows, max_suffix, scale
+    (a.q_row, a.q_head), (a.out_row, a.out_head) = _strides(q), _strides(out)
+    a.page_size, kv_heads = 1, None
+    if prefix_pages is None:
+        a.prefix_len = 0 if k_prefix is None else int(k_prefix.shape[0])
+        if prefix_len is not None and prefix_len > a.prefix_len:
+            raise QmvError(-5, f"k_prefix holds {a.prefix_len} tokens, prefix_len {prefix_len}")
+        a.prefix_len = a.prefix_len if prefix_len is None else prefix_len
+    else:
+        if prefix_len is None:
+            raise QmvError(-3, "prefix_pages without prefix_len")
+        if k_prefix is not None or v_prefix is not None:
+            raise QmvError(-3, "both prefix_pages and k_prefix or v_prefix")
+        a.prefix_len = prefix_len
+    pairs = [("k_prefix", "v_prefix", k_prefix, v_prefix, 3)] if k_prefix is not None or v_prefix is not None else []
+    if k_pages is not None or v_pages is not None:
+        pairs.append(("k_pages", "v_pages", k_pages, v_pages, 4))
+    for kn, vn, k, v, nd in pairs:
+        _check_view(k, kn, name, nd)
+        _check_view(v, vn, name, nd)
+        if k.shape != v.shape or _strides(k) != _strides(v):
+            raise QmvError(-3, f"{kn} and {vn} differ in shape or strides")
+        if k.shape[-1] != d:
+            raise QmvError(-3, f"{kn}: head width {k.shape[-1]}, expected {d}")
+        if kv_heads not in (None, int(k.shape[-2])):
+            raise QmvError(-3, f"{kn}: {k.shape[-2]} heads, expected {kv_heads}")
+        kv_heads = int(k.shape[-2])
+    a.kv_heads = heads if kv_heads is None else kv_heads
+    if k_prefix is not None:
+        a.prefix_row, a.prefix_head = _strides(k_prefix)
+    if k_pages is not None:
+        a.num_pages, a.page_size = int(k_pages.shape[0]), int(k_pages.shape[1])
+        a.page_stride, a.page_row, a.page_head = _strides(k_pages)
+    elif prefix_pages is not None or max_suffix > 0:
+        raise QmvError(-1, "k_pages is None")
+    if prefix_pages is not None:
+        _check_vec(prefix_pages, "prefix_pages", _I32, -(-prefix_len // max(1, a.page_size)))
+    if max_suffix > 0:
+        _check_view(block_table, "block_table", "int32", 2)
+        if block_table.shape[0] < nseq:
+            raise QmvError(-5, f"block_table: {block_table.shape[0]} rows, needs {nseq}")
+        if block_table.shape[1] * a.page_size < max_suffix:
+            raise QmvError(-5, f"block_table: {block_table.shape[1]} pages of {a.page_size} hold fewer than "
+                               f"{max_suffix} tokens")
+        # (one row of any stride; the library asks for a stride that covers max_suffix)
+        a.table_stride = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+        _check_vec(suffix_len, "suffix_len", _I32, nseq)
+    if tree_mask is not None:
+        _check_vec(tree_mask, "tree_mask", _I64, rows)
+    if lse is not None:
+        _check_vec(lse, "lse", _F32, rows * heads)
+    named = dict(q=q, k_prefix=k_prefix, v_prefix=v_prefix, prefix_pages=prefix_pages, k_pages=k_pages,
+                 v_pages=v_pages, block_table=block_table, row_start=row_start, suffix_len=suffix_len,
+                 tree_mask=tree_mask, out=out, lse=lse)
+    _check_one_device(list(named.items()))
+    for field, t in named.items():
+        setattr(a, field, _ptr(t))
+    a.owner = named
+    _check(lib().qmv_attn_workspace_size(ctypes.byref(a), ctypes.byref(_u64(0))))
+    return a
+
+
+def qmv_attn_workspace_size(a: QmvAttnArgs) -> int:
+    n = _u64(0)
+    _check(lib().qmv_attn_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+    return int(n.value)
+
+
+def qmv_attn(a: QmvAttnArgs, workspace, workspace_bytes: int, stream=None) -> None:
+    """Attention of the step's rows (qmv_create_attn) over the shared prefix and their sequences' suffixes."""
+    if workspace is not None:
+        _check_dev(workspace, "workspace", None, workspace_bytes)
+    owner = getattr(a, "owner", None)
+    _check(lib().qmv_attn(ctypes.byref(a), _ptr(workspace), workspace_bytes,
+                          _stream(stream, owner["q"] if owner else None, workspace)))
+
+
+def qmv_create_verify(logits, tokens, row_start, max_rows: int, u_accept, u_sample, out_tokens, accepted, *,
+                      draft_probs=None, temperature=None) -> QmvVerifyArgs:
+    """Checked arguments of qmv_verify from device tensors, kept alive with them.
+
+    logits [rows, vocab] float32, float16 or bfloat16, draft_probs [rows, vocab] float32 (rows of any stride);
+    tokens, out_tokens [rows], row_start [nseq + 1], accepted [nseq] int32; u_accept [rows], u_sample and
+    temperature [nseq] float32."""
+    a = QmvVerifyArgs()
+    name = str(getattr(logits, "dtype", "")).replace("torch.", "")
+    if name not in ("float32", "float16", "bfloat16"):
+        raise QmvError(-6, f"logits: {name or type(logits)}, expected a float32, float16 or bfloat16 tensor")
+    _check_view(logits, "logits", name, 2)
+    rows, vocab = (int(x) for x in logits.shape)
+    _check_vec(row_start, "row_start", _I32, 1)
+    nseq = int(row_start.numel()) - 1
+    if draft_probs is not None:
+        _check_view(draft_probs, "draft_probs", "float32", 2)
+        if tuple(draft_probs.shape) != (rows, vocab):
+            raise QmvError(-3, f"draft_probs: shape {tuple(draft_probs.shape)}, expected {(rows, vocab)}")
+        a.draft_row = draft_probs.stride(0) if rows > 1 else vocab
+    for what, t, kind, n in [("tokens", tokens, _I32, rows), ("u_accept", u_accept, _F32, rows),
+                             ("u_sample", u_sample, _F32, nseq), ("out_tokens", out_tokens, _I32, rows),
+                             ("accepted", accepted, _I32, nseq)]:
+        _check_vec(t, what, kind, n)
+    if temperature is not None:
+        _check_vec(temperature, "temperature", _F32, nseq)
+    a.logits_dtype, a.nseq, a.max_rows, a.rows, a.vocab = _dtype(logits.dtype), nseq, max_rows, rows, vocab
+    a.logits_row = logits.stride(0) if rows > 1 else vocab
+    named = dict(logits=logits, draft_probs=draft_probs, tokens=tokens, row_start=row_start, temperature=temperature,
+                 u_accept=u_accept, u_sample=u_sample, out_tokens=out_tokens, accepted=accepted)
+    _check_one_device(list(named.items()))
+    for field, t in named.items():
+        setattr(a, field, _ptr(t))
+    a.owner = named
+    _check(lib().qmv_verify_workspace_size(ctypes.byref(a), ctypes.byref(_u64(0))))
+    return a
+
+
+def qmv_verify_workspace_size(a: QmvVerifyArgs) -> int:
+    n = _u64(0)
+    _check(lib().qmv_verify_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+    return int(n.value)
+
+
+def qmv_verify(a: QmvVerifyArgs, workspace, workspace_bytes: int, stream=None) -> None:
+    """Drafted tokens checked against the target's probabilities (qmv_create_verify)."""
+    if workspace is not None:
+        _check_dev(workspace, "workspace", None, workspace_bytes)
+    owner = getattr(a, "owner", None)
+    _check(lib().qmv_verify(ctypes.byref(a), _ptr(workspace), workspace_bytes,
+                            _stream(stream, owner["logits"] if owner else None, workspace)))
 
 
 def qmv_probe_read_outputs(nbytes: int) -> int:

@@ -366,6 +366,147 @@ int32_t qmv_gemv_swiglu(int32_t fmt, const qmv_weights* Wg,
 int32_t qmv_dequant(const qmv_weights* W, void* out, int32_t out_dtype,
                     void* stream);
 
+/* out[i] = scale * W[ids[i]] for n token ids: rows of a block-quantized
+ * embedding table (in GGUF files often the lm-head's own matrix), looked up on
+ * the device.  W is rows x cols in any format and layout; ids holds n int32
+ * row numbers in device memory (4-byte aligned); out is [n][cols] of out_dtype
+ * (QMV_F32, QMV_F16 or QMV_BF16, 16-byte aligned).  Each value is the exact
+ * weight rounded to fp32 (as qmv_dequant), times scale rounded to fp32, then
+ * rounded to out_dtype (nearest even).  An id outside [0, rows) -- the -1 that
+ * qmv_verify leaves where a sequence has no token -- gives a row of zeros and
+ * reads nothing.  n = 0 launches nothing; n < 0 is QMV_ERR_SHAPE.  A quantized
+ * table is frozen, so the lookup has no gradient.  Enqueues only; no
+ * workspace; legal inside HIP stream capture. */
+int32_t qmv_embed(const qmv_weights* W, const int32_t* ids, int64_t n,
+                  float scale, void* out, int32_t out_dtype, void* stream);
+
+/* ---- Attention and verification of a draft-and-verify decode step ------
+ * Both calls take the step's rows of all sequences at once: sequence b
+ * (0 <= b < nseq) has rows row_start[b] .. row_start[b + 1], the first for its
+ * last accepted token and one more for each token drafted after it (one row
+ * per sequence in plain decode).  row_start is nondecreasing; a sequence may
+ * have no rows.  Device-side integers are not visible to the checks here: the
+ * kernels clamp them, so that no value makes them read or write outside the
+ * buffers described by the host-side fields. */
+
+/* Arguments of qmv_attn.  Strides count elements and are multiples of 8;
+ * pointers to q, k, v and out are 16-byte aligned, the others by their type. */
+typedef struct qmv_attn_args {
+  int32_t dtype;        /* QMV_F16 or QMV_BF16: q, k, v and out              */
+  int32_t head_dim;     /* D: a multiple of 8, 8..256                        */
+  int32_t heads;        /* query heads, a multiple of kv_heads               */
+  int32_t kv_heads;     /* query head h reads key head h / (heads/kv_heads)  */
+  int32_t nseq;
+  int32_t max_rows;     /* most rows of a sequence                           */
+  int32_t page_size;    /* tokens per page: a power of two, 1..65536         */
+  float scale;          /* score = scale * (q . k); positive and finite      */
+  int64_t rows;         /* rows of q and out                                 */
+  int64_t prefix_len;   /* tokens of the prefix that every row sees          */
+  int64_t max_suffix;   /* most suffix tokens of a sequence                  */
+  int64_t num_pages;    /* pages in the pool                                 */
+  int64_t table_stride; /* entries from one row of block_table to the next   */
+  int64_t q_row, q_head;           /* q[row][head][D]                        */
+  int64_t out_row, out_head;       /* out[row][head][D]                      */
+  int64_t prefix_row, prefix_head; /* k_prefix, v_prefix [token][kv head][D] */
+  int64_t page_stride, page_row, page_head; /* k_pages, v_pages              */
+                                   /* [page][token][kv head][D]              */
+  const void* q;
+  const void* k_prefix;  /* the prefix, contiguous in tokens; unused where   */
+  const void* v_prefix;  /* prefix_pages is given or prefix_len is 0         */
+  const int32_t* prefix_pages; /* NULL, or the prefix's pages in the pool    */
+  const void* k_pages;   /* page pool of the suffixes                        */
+  const void* v_pages;
+  const int32_t* block_table;  /* [nseq][table_stride] page numbers          */
+  const int32_t* row_start;    /* [nseq + 1]                                 */
+  const int32_t* suffix_len;   /* [nseq] tokens, the sequence's rows among   */
+                               /* them as its last ones                      */
+  const uint64_t* tree_mask;   /* NULL, or [rows]: bit i of a row's mask     */
+                               /* says that it sees its sequence's row i     */
+  void* out;
+  float* lse;            /* NULL, or [rows][heads]: log of the sum of e^score */
+} qmv_attn_args;
+
+/* out = softmax(scale q k) v over the shared prefix and then the row's own
+ * sequence: row i of a sequence with n rows and s suffix tokens sees every
+ * prefix token, the s - n suffix tokens before its sequence's rows, and of
+ * those rows the ones up to itself (or, with tree_mask, the ones whose bit is
+ * set: a draft tree; max_rows <= 64).  The prefix is read once for all rows of
+ * a key head together, not once per sequence.  A key on a page number outside
+ * [0, num_pages) is not seen.  What no row sees (stale tokens of a page, the
+ * keys above) may hold anything, infinities and NaN among them.  A row that
+ * sees no key gives zeros and lse = -inf.  A row outside every sequence sees
+ * the prefix alone; a row past its sequence's max_rows is filled with NaN; a
+ * suffix longer than max_suffix is cut there.
+ * Scores, maxima, sums and outputs are held in fp32; the probabilities enter
+ * the second product as two values of q's type that together hold 16 bits or
+ * more.  Keys are split over workgroups whose partial results (in the
+ * workspace) are joined in a fixed order: results do not depend on timing.
+ * Inference only: no gradient.
+ * workspace as in qmv_gemv_multi_ws: 256-byte aligned, at least
+ * qmv_attn_workspace_size bytes (QMV_ERR_SIZE), no initial value.  rows = 0
+ * launches nothing.  Errors: QMV_ERR_NULL, QMV_ERR_SHAPE (counts, heads not a
+ * multiple of kv_heads, page_size, strides), QMV_ERR_SIZE (table_stride too
+ * small for max_suffix), QMV_ERR_ALIGN, QMV_ERR_RANGE (scale),
+ * QMV_ERR_UNSUPPORTED (dtype, head_dim, sizes past the limits, tree_mask with
+ * max_rows > 64).  Enqueues only; legal inside HIP stream capture. */
+int32_t qmv_attn_workspace_size(const qmv_attn_args* a, uint64_t* bytes);
+int32_t qmv_attn(const qmv_attn_args* a, void* workspace,
+                 uint64_t workspace_bytes, void* stream);
+
+/* Arguments of qmv_verify.  Pointers aligned by their type. */
+typedef struct qmv_verify_args {
+  int32_t logits_dtype;  /* QMV_F32, QMV_F16 or QMV_BF16                     */
+  int32_t nseq;
+  int32_t max_rows;      /* most rows of a sequence                          */
+  int32_t reserved;      /* 0                                                */
+  int64_t rows;          /* rows of logits, tokens, u_accept and out_tokens  */
+  int64_t vocab;         /* 1..2^24                                          */
+  int64_t logits_row;    /* elements from one row of logits to the next      */
+  int64_t draft_row;     /* the same of draft_probs                          */
+  const void* logits;          /* [rows][vocab] the target's                 */
+  const float* draft_probs;    /* NULL, or [rows][vocab]: row r holds the    */
+                               /* probabilities from which tokens[r + 1] was */
+                               /* drafted; a sequence's last row is not read */
+  const int32_t* tokens;       /* [rows] the rows' tokens                    */
+  const int32_t* row_start;    /* [nseq + 1]                                 */
+  const float* temperature;    /* NULL (1), or [nseq]; 0: the likeliest token */
+  const float* u_accept;       /* [rows] uniform numbers in [0, 1)           */
+  const float* u_sample;       /* [nseq] uniform numbers in [0, 1)           */
+  int32_t* out_tokens;         /* [rows]                                     */
+  int32_t* accepted;           /* [nseq]                                     */
+} qmv_verify_args;
+
+/* Verification of drafted tokens by rejection sampling with given random
+ * numbers: the tokens that come out are distributed as the target's.  With
+ * p = softmax(logits[r] / temperature) and q = draft_probs[r] (one at the
+ * drafted token and zero elsewhere where draft_probs is NULL), the draft
+ * x = tokens[r + 1] is accepted where u_accept[r] q(x) < p(x); the first row
+ * of a sequence whose draft is not accepted draws its token from
+ * max(p - q, 0) / sum instead (from p, where that is zero everywhere), and a
+ * sequence whose drafts are all accepted draws one more from its last row's p.
+ * A draw takes the lowest token i with sum_{j <= i} w_j > u_sample * sum_j w_j.
+ * Temperature 0: p is one at the largest logit, the lowest index of equal
+ * ones, and q is taken as one at x.  accepted[b] = accepted drafts;
+ * out_tokens holds, at the sequence's rows, the accepted drafts, the drawn
+ * token and then -1 (rows outside every sequence: -1).  A row that draws
+ * without drafts (a sequence of one row) is an ordinary sampling step.
+ * NaN logits count as -inf; a row of nothing but -inf has no distribution:
+ * its draft is not accepted and it draws -1.  A row with +inf logits shares
+ * its probability among them.  A draft outside [0, vocab) is not accepted;
+ * NaN and negative draft probabilities count as zero; a negative or NaN
+ * temperature counts as 0.
+ * Exponentials, sums and comparisons are in 64 bits, and sums are added in a
+ * fixed order: results do not depend on timing, and a draw differs from exact
+ * arithmetic only within about 1e-12 of a border between two tokens.
+ * Sequences of more than max_rows rows have the rows past it treated as not
+ * there.  workspace as in qmv_attn.  rows = 0 launches nothing if nseq is 0
+ * too.  Errors: QMV_ERR_NULL, QMV_ERR_SHAPE (counts, row strides below
+ * vocab), QMV_ERR_ALIGN, QMV_ERR_SIZE, QMV_ERR_UNSUPPORTED (dtype, vocab).
+ * Enqueues only; legal inside HIP stream capture. */
+int32_t qmv_verify_workspace_size(const qmv_verify_args* a, uint64_t* bytes);
+int32_t qmv_verify(const qmv_verify_args* a, void* workspace,
+                   uint64_t workspace_bytes, void* stream);
+
 /* Measurement kernels for the HBM roofline (not part of the GEMV path).
  * qmv_probe_read streams nbytes (multiple of 16) from src with nontemporal
  * 128-bit loads, one contiguous chunk per workgroup (the fastest streaming
