@@ -30,7 +30,8 @@ CXX_SOURCES = ["packer.cpp"]
 # Per-source device flags.  The matrix-core kernels scale each product in
 # VALU right away; in accumulation registers every result would need a
 # v_accvgpr_read first, so their results are kept in ordinary VGPRs.
-SOURCE_FLAGS = {"gemm_q4_k_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+SOURCE_FLAGS = {"gemm_q4_k_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _run(cmd, verbose):

@@ -167,6 +167,7 @@ static int32_t check_attn(const qmv_attn_args* a) {
                         static_cast<const void*>(a->lse)})
     if (!aligned_to(p, 4)) return fail(QMV_ERR_ALIGN, "an int32 or fp32 pointer is not 4-byte aligned");
   if (!aligned_to(a->tree_mask, 8)) return fail(QMV_ERR_ALIGN, "tree_mask not 8-byte aligned");
+  if (!attn_fits(*a)) return fail(QMV_ERR_UNSUPPORTED, "more key ranges than a launch has workgroups");
   return QMV_OK;
 }
 

@@ -166,6 +166,7 @@ hipError_t embed(const qmv_weights& W, const int32_t* ids, int64_t n, float scal
 
 // Attention over a shared prefix and paged suffixes (attn.hip) and the
 // verification of drafted tokens (verify.hip), after validation.
+bool attn_fits(const qmv_attn_args& a);  // within a launch's workgroups
 size_t attn_workspace(const qmv_attn_args& a);
 hipError_t attn(const qmv_attn_args& a, void* ws, hipStream_t s);
 size_t verify_workspace(const qmv_verify_args& a);
