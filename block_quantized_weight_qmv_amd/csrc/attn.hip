@@ -21,9 +21,11 @@
 //
 // K and V tiles go from memory to LDS without passing registers.  16-byte
 // chunks of a tile's row are permuted by the row's number so that neither
-// product's reads meet in a bank (swz_k, swz_v); the copy fills LDS in order,
+// product's reads meet in a bank (swz); the copy fills LDS in order,
 // so each lane asks for the chunk that belongs at its place.
 #include <float.h>
+
+#include <algorithm>
 
 #include "device_util.h"
 #include "launch.h"
@@ -46,8 +48,8 @@ constexpr float kNone = -FLT_MAX;
 // fp32 or in the second product's types, and the 32..128 outputs of a lane
 // need no rescaling.
 constexpr float kSlack = 8.f;
-// Keys of one workgroup where they lie in pages: their page numbers are held in LDS.
-constexpr int kMaxPagedKeys = 2048;
+// Pages of one workgroup's keys: their numbers are held in LDS.
+constexpr int kMaxPages = 2048;
 
 // Where the keys of a workgroup come from.
 struct KeySource {
@@ -59,8 +61,27 @@ struct KeySource {
   int shift, npages;      // log2 of the page size
 };
 
+// n / d for 0 <= n < 2^31, as a multiplication (Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication", 1994).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+
+static FastDiv fast_div(int64_t d) {
+  FastDiv f{static_cast<uint32_t>(d), 0, 0};
+  while ((int64_t{1} << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << f.shift) - d)) / d + 1);
+  return f;
+}
+
+__device__ __forceinline__ int quotient(int n, const FastDiv& f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.mul) + static_cast<uint32_t>(n)) >> f.shift);
+}
+__device__ __forceinline__ int remainder_of(int n, int q, const FastDiv& f) { return n - q * static_cast<int>(f.d); }
+
 struct AttnPlan {
   int groups;        // query heads per key head
+  int suffix_first;  // the suffixes' workgroups run longer: they are launched first
   int wide;          // prefix: 128-row tiles of four waves (else 32-row tiles, four waves along the keys)
   int row_tiles;     // prefix row tiles per key head
   int psplits, pseg; // prefix key ranges and their keys
@@ -73,19 +94,16 @@ struct AttnPlan {
 struct AttnKernelArgs {
   qmv_attn_args a;
   AttnPlan p;
+  FastDiv groups, pairs, kv_heads, srow_tiles, ssplits, heads;
   float* po;         // [slot][row * heads + head][D]
   float2* pml;       // [slot][row * heads + head]: maximum (log2), sum
 };
 
-// What tokens past a range's end and pages outside the pool are read from.
-__device__ const uint4 g_zero_row[32] = {};
-
+// The permutation of a tile row's 16-byte chunks.  Of the eight rows that a
+// first-product read takes at one chunk, and of the four rows x two chunks of
+// a transposing read, none share a bank.
 template <int DP>
-__device__ __forceinline__ int swz_k(int row) {
-  return DP == 64 ? (row >> 1) & 7 : row & 7;
-}
-template <int DP>
-__device__ __forceinline__ int swz_v(int row) {
+__device__ __forceinline__ int swz(int row) {
   return DP == 64 ? ((row >> 1) & 3) * 2 : (row & 7) * 2;
 }
 
@@ -171,7 +189,7 @@ struct RowTile {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
       const lds_u8* row = kt + (t * 32 + r) * ROWB;
-      const int z = swz_k<DP>(r);
+      const int z = swz<DP>(r);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const u32x4 kf = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(row + (((2 * ks + h) ^ z) << 4));
@@ -233,9 +251,9 @@ struct RowTile {
           const int ch = 4 * dt + 2 * g + (b >> 1), in = (b & 1) * 8;
           typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
           const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4*)(vt + r0 * ROWB + ((ch ^ swz_v<DP>(r0)) << 4) + in));
+              (lds_i16x4*)(vt + r0 * ROWB + ((ch ^ swz<DP>(r0)) << 4) + in));
           const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4*)(vt + (r0 + 8) * ROWB + ((ch ^ swz_v<DP>(r0 + 8)) << 4) + in));
+              (lds_i16x4*)(vt + (r0 + 8) * ROWB + ((ch ^ swz<DP>(r0 + 8)) << 4) + in));
           const uint2 w0 = __builtin_bit_cast(uint2, v0), w1 = __builtin_bit_cast(uint2, v1);
           const u32x4 vf = {w0.x, w0.y, w1.x, w1.y};
           o[dt] = mfma<BF>(vf, hi, o[dt]);
@@ -245,44 +263,62 @@ struct RowTile {
   }
 };
 
-// Copies of one tile: this wave's NI instructions of 64 / CPR rows each, from
-// row `row0` of the tile at LDS address `lds`, whose row 0 is key `key0`;
-// keys from `end` on, and keys of pages outside the pool, are zeros.
-template <int DP, int NI, bool ISV>
+// Copies of this wave's NI instructions of a tile, 64 / CPR rows each, from
+// row `row0` of the tile on; K and V lie alike, so one set of offsets serves
+// both.
+template <int DP, int NI>
 struct TileCopy {
   static constexpr int CPR = DP / 8, RPI = 64 / CPR;
-  uint32_t off[NI];  // contiguous tokens: byte offset from the tile's first token
+  static constexpr int NV = RPI >= 8 ? 1 : 8 / RPI;  // instructions until the permutation repeats
+  uint32_t off[NV];  // this lane's bytes from the instruction's first row
 
   __device__ __forceinline__ static int chunk(int row, int lane, int D) {
-    const int ch = (lane % CPR) ^ (ISV ? swz_v<DP>(row) : swz_k<DP>(row));
+    const int ch = (lane % CPR) ^ swz<DP>(row);
     return ch * 8 < D ? ch : 0;  // (columns past D: anything of the row; they meet zeros of q, or are not stored)
   }
-  __device__ __forceinline__ void init(const KeySource& src, int row0, int lane, int D) {
+  // (row0 is a multiple of 8)
+  __device__ __forceinline__ void init(const KeySource& src, int lane, int D) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int row = row0 + i * RPI + lane / CPR;
-      off[i] = static_cast<uint32_t>(row * static_cast<uint32_t>(src.row)) + chunk(row, lane, D) * 16;
-    }
+    for (int i = 0; i < NV; ++i)
+      off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + chunk(i * RPI + lane / CPR, lane, D) * 16;
   }
-  __device__ __forceinline__ void fast(const uint8_t* tile, int row0, uint32_t lds) const {
+  // Key key0 is the tile's row 0.  Rows past the last key before `end` repeat
+  // it, and keys of pages outside the pool are page 0's: what they hold is not
+  // used.  each: every instruction's rows lie in one page of the pool (or
+  // tokens are contiguous) and `off` holds.
+  __device__ __forceinline__ void copy(const KeySource& src, const uint8_t* base, const int* pages, int first, bool each,
+                                       int key0, int end, int row0, uint32_t lds, int lane, int D) const {
+    const int in_page = (1 << src.shift) - 1;
+    if (each) {
+      // lane r: where row r begins; an instruction takes its first row's
+      const int mine = min(key0 + row0 + lane, end - 1);
+      int64_t at = mine * src.row;
+      if (pages) at = max(pages[(mine >> src.shift) - first], 0) * src.page + (mine & in_page) * src.row;
+      const uint64_t from = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(at);
+      const auto start = [&](int i) {
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(from), i * RPI);
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(from >> 32), i * RPI);
+        return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
+      };
+      if (key0 + row0 + NI * RPI <= end) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) copy_to_lds(tile, off[i], lds + (row0 + i * RPI) * DP * 2);
-  }
-  __device__ __forceinline__ static void slow(const KeySource& src, const uint8_t* base, const int* pages, int first,
-                                              int key0, int end, int row0, uint32_t lds, int lane, int D) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int row = row0 + i * RPI + lane / CPR, key = key0 + row, ch = chunk(row, lane, D);
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(g_zero_row);
-      if (key < end) {
-        if (pages) {
-          const int pg = pages[(key >> src.shift) - first];
-          if (pg >= 0) p = base + pg * src.page + (key & ((1 << src.shift) - 1)) * src.row;
-        } else {
-          p = base + key * src.row;
+        for (int i = 0; i < NI; ++i) copy_to_lds(start(i), off[i % NV], lds + (row0 + i * RPI) * DP * 2);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i) {
+          const int row = row0 + i * RPI, have = max(end - 1 - (key0 + row), 0);
+          const uint32_t o = static_cast<uint32_t>(min(lane / CPR, have)) * static_cast<uint32_t>(src.row) +
+                             chunk(row + lane / CPR, lane, D) * 16;
+          copy_to_lds(start(i), o, lds + row * DP * 2);
         }
       }
-      copy_to_lds(p + ch * 16, lds + (row0 + i * RPI) * DP * 2);
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      const int row = row0 + i * RPI + lane / CPR, key = min(key0 + row, end - 1);
+      const int64_t page = pages ? max(pages[(key >> src.shift) - first], 0) : 0, in = pages ? key & in_page : key;
+      copy_to_lds(base + page * src.page + in * src.row + chunk(row, lane, D) * 16, lds + (row0 + i * RPI) * DP * 2);
     }
   }
 };
@@ -307,11 +343,22 @@ __device__ __forceinline__ int key_of(int i, int lane) { return 8 * (i >> 2) + 4
 template <bool BF, int DP>
 struct Attn {
   typedef RowTile<BF, DP> Tile;
+
+  // Whether a copy instruction's rows have one base address and 32-bit offsets.
+  static __device__ __forceinline__ bool copies_by_instruction(const KeySource& src, bool bad) {
+    return !bad && src.row < (int64_t{1} << 28) && (!src.table || (1 << src.shift) >= RPI);
+  }
+
   static constexpr int CPR = DP / 8, RPI = 64 / CPR, ROWB = DP * 2;
   static constexpr int kWideKeys = DP == 256 ? 32 : 64;        // keys of a wide tile
   static constexpr int kTileBytes = kWideKeys * ROWB;          // its K or V
   static constexpr int kWaveBytes = 32 * ROWB;                 // narrow: a wave's K or V
   static constexpr int kLds = 4 * kTileBytes > 8 * kWaveBytes ? 4 * kTileBytes : 8 * kWaveBytes;
+
+  static __device__ __forceinline__ void zero_chunk(lds_u8* at) {
+    const u32x4 z = {0, 0, 0, 0};
+    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = z;
+  }
 
   // The unnormalized output of a lane's row to the workspace (wide).
   static __device__ __forceinline__ void store(const Tile& t, float* po, float2* pml, int D, int lane) {
@@ -337,45 +384,45 @@ struct Attn {
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
     const int G = g.p.groups, M = static_cast<int>(a.rows) * G;
     const int m0 = rt * 128 + wave * 32, mi = min(m0 + (lane & 31), M - 1);
-    const int row = mi / G, head = hk * G + mi % G;
-    Tile t;
-    t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
+    const int row = quotient(mi, g.groups), head = hk * G + remainder_of(mi, row, g.groups);
     bool bad = false;
     if (src.table) bad = load_pages(src, k0, k1, pages);
     const int first = src.table ? k0 >> src.shift : 0;
     const int* pg = src.table ? pages : nullptr;
     constexpr int NI = kWideKeys / 4 / RPI;
     const int row0 = wave * (kWideKeys / 4);
-    TileCopy<DP, NI, false> ck;
-    TileCopy<DP, NI, true> cv;
-    ck.init(src, row0, lane, D);
-    cv.init(src, row0, lane, D);
-    const bool plain = !src.table && src.row < (int64_t{1} << 25);
+    TileCopy<DP, NI> cp;
+    cp.init(src, lane, D);
+    const bool each = copies_by_instruction(src, bad);
     const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)smem));
+    const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + kWideKeys - 1) / kWideKeys;
+    constexpr int NT = kWideKeys / 32;
     auto copy = [&](int tile) {
       const int key0 = k0 + tile * kWideKeys;
       const uint32_t at = lds + (tile & 1) * 2 * kTileBytes;
-      if (plain && key0 + kWideKeys <= k1) {
-        ck.fast(src.k + key0 * src.row, row0, at);
-        cv.fast(src.v + key0 * src.row, row0, at + kTileBytes);
-      } else {
-        ck.slow(src, src.k, pg, first, key0, k1, row0, at, lane, D);
-        cv.slow(src, src.v, pg, first, key0, k1, row0, at + kTileBytes, lane, D);
-      }
+      cp.copy(src, src.k, pg, first, each, key0, k1, row0, at, lane, D);
+      cp.copy(src, src.v, pg, first, each, key0, k1, row0, at + kTileBytes, lane, D);
     };
-    const int tiles = (k1 - k0 + kWideKeys - 1) / kWideKeys;
-    constexpr int NT = kWideKeys / 32;
-    copy(0);
+    if (tiles) copy(0);
+    Tile t;
+    t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
 #pragma unroll 1
     for (int tile = 0; tile < tiles; ++tile) {
       wait_copies<0>();
       lds_barrier();
       if (tile + 1 < tiles) copy(tile + 1);
+      lds_u8* kt = (lds_u8*)smem + (tile & 1) * 2 * kTileBytes;
+      const int left = k1 - k0 - tile * kWideKeys;
+      if (left < kWideKeys || bad) {
+        // values of keys that are not there: 0 x infinity or NaN is not 0
+        for (int r = threadIdx.x / CPR; r < kWideKeys; r += 256 / CPR)
+          if (r >= left || (bad && pages[((k0 + tile * kWideKeys + r) >> src.shift) - first] < 0))
+            zero_chunk(kt + kTileBytes + r * ROWB + threadIdx.x % CPR * 16);
+        lds_barrier();
+      }
       if (m0 >= M) continue;  // (whole waves: they only copy)
-      const lds_u8* kt = (const lds_u8*)smem + (tile & 1) * 2 * kTileBytes;
       f32x16 s[NT];
       t.template scores<NT>(kt, lane, s);
-      const int left = k1 - k0 - tile * kWideKeys;
       if (left < kWideKeys || bad) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -407,67 +454,61 @@ struct Attn {
     const qmv_attn_args& a = g.a;
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
     const int G = g.p.groups, M = nrows * G;
-    const int mi = min(r0 + (lane & 31), M - 1);
-    const int row = rbase + mi / G, head = hk * G + mi % G;
-    Tile t;
-    t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
-    const uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
+    const int mi = min(r0 + (lane & 31), M - 1), ri = quotient(mi, g.groups);
+    const int row = rbase + ri, head = hk * G + remainder_of(mi, ri, g.groups);
     bool bad = false;
     if (src.table) bad = load_pages(src, k0, k1, pages);
     const int first = src.table ? k0 >> src.shift : 0;
     const int* pg = src.table ? pages : nullptr;
     constexpr int NI = 32 / RPI;
-    TileCopy<DP, NI, false> ck;
-    TileCopy<DP, NI, true> cv;
-    ck.init(src, 0, lane, D);
-    cv.init(src, 0, lane, D);
-    const bool plain = !src.table && src.row < (int64_t{1} << 25);
+    TileCopy<DP, NI> cp;
+    cp.init(src, lane, D);
+    const bool each = copies_by_instruction(src, bad);
     lds_u8* kt = (lds_u8*)smem + wave * 2 * kWaveBytes;
     lds_u8* vt = kt + kWaveBytes;
     const uint32_t klds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt)), vlds = klds + kWaveBytes;
-    auto copy_k = [&](int tile) {
-      const int key0 = k0 + tile * 32;
-      if (plain && key0 + 32 <= k1) ck.fast(src.k + key0 * src.row, 0, klds);
-      else ck.slow(src, src.k, pg, first, key0, k1, 0, klds, lane, D);
-    };
-    auto copy_v = [&](int tile) {
-      const int key0 = k0 + tile * 32;
-      if (plain && key0 + 32 <= k1) cv.fast(src.v + key0 * src.row, 0, vlds);
-      else cv.slow(src, src.v, pg, first, key0, k1, 0, vlds, lane, D);
-    };
-    const int tiles = (k1 - k0 + 31) / 32;
+    const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + 31) / 32;
     if (wave < tiles) {
-      copy_k(wave);
-      copy_v(wave);
+      cp.copy(src, src.k, pg, first, each, k0 + wave * 32, k1, 0, klds, lane, D);
+      cp.copy(src, src.v, pg, first, each, k0 + wave * 32, k1, 0, vlds, lane, D);
     }
+    Tile t;
+    t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
+    const uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
 #pragma unroll 1
     for (int tile = wave; tile < tiles; tile += 4) {
       const int key0 = k0 + tile * 32;
+      const bool more = tile + 4 < tiles;
       f32x16 s[1];
-      wait_copies<NI>();
+      wait_copies<NI>();  // outstanding: this tile's K, its V
       t.template scores<1>(kt, lane, s);
       wait_lds();
-      copy_k(tile + 4);  // (past the last tile: zeros that nobody reads)
-      const bool drafts = key0 + 32 > draft0;
-      if (drafts || key0 + 32 > k1 || bad) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = key0 + key_of(i, lane);
-          bool seen = j < k1;
-          const int at = j - draft0;
-          if (at >= 0) seen = seen && (a.tree_mask ? at < 64 && ((mask >> (at & 63)) & 1) : at <= row - rbase);
-          if (bad && seen) seen = pages[(j >> src.shift) - first] >= 0;
-          s[0][i] = seen ? s[0][i] : -INFINITY;
+      if (more) cp.copy(src, src.k, pg, first, each, key0 + 128, k1, 0, klds, lane, D);
+      const bool partly = key0 + 32 > min(draft0, k1) || bad;  // some rows do not see some of the keys
+      if (partly) {
+        // bit j: the lane's row sees key key0 + j
+        const int left = k1 - key0, at = draft0 - key0;
+        uint32_t seen = left >= 32 ? ~0u : (1u << left) - 1;
+        if (a.tree_mask)
+          seen &= at >= 32 ? ~0u : at >= 0 ? ((1u << at) - 1) | static_cast<uint32_t>(mask << at)
+                                           : at > -64 ? static_cast<uint32_t>(mask >> -at) : 0u;
+        else
+          seen &= at + ri >= 31 ? ~0u : at + ri >= 0 ? (2u << (at + ri)) - 1 : 0u;
+        if (bad) {
+          const int key = min(key0 + (lane & 31), k1 - 1);
+          seen &= ~static_cast<uint32_t>(__ballot(pages[(key >> src.shift) - first] < 0));
         }
+        seen >>= 4 * (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[0][i] = (seen >> (8 * (i >> 2) + (i & 3))) & 1 ? s[0][i] : -INFINITY;
       }
       t.template softmax<1>(s);
-      wait_copies<NI>();
-      if (drafts) unseen_values(t, s[0], vt, lane, max(draft0 - key0, 0), D);
+      if (more) wait_copies<NI>(); else wait_copies<0>();
+      if (partly) unseen_values(t, s[0], vt, lane, bad ? 0 : min(draft0, k1) - key0, D);
       t.template values<1>(vt, lane, s);
       wait_lds();
-      copy_v(tile + 4);
+      if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane, D);
     }
-    wait_copies<0>();
     __syncthreads();
 
     // The waves' parts: [wave][row][DP] in the tiles' place, maxima and sums in `pages`.
@@ -487,9 +528,9 @@ struct Attn {
     }
     __syncthreads();
     constexpr int kQuads = DP / 4;
-    for (int e = threadIdx.x; e < 32 * kQuads; e += 256) {
+    for (int e = threadIdx.x; e < min(32, M - r0) * kQuads; e += 256) {
       const int r = e / kQuads, ch = e % kQuads, m = r0 + r;
-      if (m >= M || ch * 4 >= D) continue;
+      if (ch * 4 >= D) continue;
       float2 w[4];
       float mx = kNone;
 #pragma unroll
@@ -509,29 +550,34 @@ struct Attn {
         sum.w = fmaf(f, v.w, sum.w);
         sl = fmaf(f, w[k].y, sl);
       }
-      const size_t at = static_cast<size_t>(slot) * a.rows * a.heads +
-                        static_cast<size_t>(rbase + m / G) * a.heads + hk * G + m % G;
+      const int mr = quotient(m, g.groups);
+      const size_t at = static_cast<size_t>(slot) * a.rows * a.heads + static_cast<size_t>(rbase + mr) * a.heads +
+                        hk * G + remainder_of(m, mr, g.groups);
       *reinterpret_cast<float4*>(g.po + at * D + ch * 4) = sum;
       if (ch == 0) g.pml[at] = make_float2(mx, sl);
     }
   }
 
-  // Drafted keys are seen by some of the rows only, and 0 x infinity or NaN is
-  // not 0: values of tile rows from `from` on that are not finite are added
-  // here to the rows that see them, and zeroed for the product.
+  // Drafted keys are seen by some of the rows only (and keys past the range's
+  // end or on pages outside the pool by none), and 0 x infinity or NaN is not
+  // 0: values of tile rows from `from` on that are not finite are added here
+  // to the rows that see them, and zeroed for the product.
   static __device__ __forceinline__ void unseen_values(Tile& t, const f32x16& p, lds_u8* vt, int lane, int from,
                                                        int D) {
     const int r = lane & 31;
-    constexpr uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
-    bool odd = false;
-#pragma unroll 1
-    for (int ch = lane >> 5; ch * 8 < D; ch += 2) {
-      const u32x4 w = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
-          vt + r * ROWB + ((ch ^ swz_v<DP>(r)) << 4));
+    constexpr uint16_t kExp = BF ? 0x7F80u : 0x7C00u;  // (columns past D, where D is not DP, are some of the row's)
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u32x4 w[CPR / 2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        odd |= (w[k] & kExp) == kExp || ((w[k] >> 16) & kExp) == kExp;
-    }
+    for (int k = 0; k < CPR / 2; ++k)
+      w[k] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(vt + r * ROWB + ((2 * k + (lane >> 5)) << 4));
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int k = 0; k < CPR / 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[k][i] & 0x7FFF7FFFu));
+    const bool odd = top.x >= kExp || top.y >= kExp;
     const uint64_t all = __ballot(odd && r >= from);
     uint32_t rows = static_cast<uint32_t>(all | (all >> 32));
     while (rows) {
@@ -550,15 +596,12 @@ struct Attn {
         for (int i = 0; i < 16; ++i) {
           const int d = 32 * dt + key_of(i, lane);
           const uint32_t b = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
-              vt + kk * ROWB + (((d >> 3) ^ swz_v<DP>(kk)) << 4) + (d & 7) * 2);
+              vt + kk * ROWB + (((d >> 3) ^ swz<DP>(kk)) << 4) + (d & 7) * 2);
           const float v = BF ? bf16_to_f32(b) : f16_to_f32(b);
           t.o[dt][i] = seen ? fmaf(pk, v, t.o[dt][i]) : t.o[dt][i];
         }
       order_memory();
-      if (lane < CPR) {
-        const u32x4 z = {0, 0, 0, 0};
-        *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(vt + kk * ROWB + lane * 16) = z;
-      }
+      if (lane < CPR) zero_chunk(vt + kk * ROWB + lane * 16);
       order_memory();
     }
   }
@@ -576,103 +619,159 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(cons
   src.npages = static_cast<int>(a.num_pages);
   src.page = a.page_stride * 2;
   int id = blockIdx.x;
-  const int before = static_cast<int>(g.p.prefix_wgs);
-  if (id < before) {
+  const int before = static_cast<int>(g.p.suffix_first ? g.p.suffix_wgs : g.p.prefix_wgs);
+  const bool prefix = (id < before) != (g.p.suffix_first != 0);
+  if (id >= before) id -= before;
+  int hk, rt, slot, k0, k1, rbase = 0, n = static_cast<int>(a.rows), draft0;
+  if (prefix) {
     // workgroups of one key head and key range are a multiple of 8 apart where
     // there are a multiple of 8 such pairs: on one XCD, sharing its L2
-    const int pairs = a.kv_heads * g.p.psplits;
-    const int rt = id / pairs, pair = id % pairs;
-    const int hk = pair % a.kv_heads, split = pair / a.kv_heads;
-    const int k0 = split * g.p.pseg, k1 = min(k0 + g.p.pseg, static_cast<int>(a.prefix_len));
+    rt = quotient(id, g.pairs);
+    const int pair = remainder_of(id, rt, g.pairs);
+    slot = quotient(pair, g.kv_heads);
+    hk = remainder_of(pair, slot, g.kv_heads);
+    k0 = slot * g.p.pseg;
+    k1 = draft0 = min(k0 + g.p.pseg, static_cast<int>(a.prefix_len));
     src.table = a.prefix_pages;
-    src.k = static_cast<const uint8_t*>(src.table ? a.k_pages : a.k_prefix) + hk * (src.table ? a.page_head : a.prefix_head) * 2;
-    src.v = static_cast<const uint8_t*>(src.table ? a.v_pages : a.v_prefix) + hk * (src.table ? a.page_head : a.prefix_head) * 2;
-    src.row = (src.table ? a.page_row : a.prefix_row) * 2;
-    if (g.p.wide)
-      A::wide(g, src, split, hk, rt, k0, k1, attn_lds, pages);
-    else
-      A::narrow(g, src, split, hk, 0, static_cast<int>(a.rows), rt * 32, k0, k1, k1, attn_lds, pages);
-    return;
+  } else {
+    // a sequence's key heads share lines: 8 x kv_heads workgroups go to the 8
+    // XCDs as 8 sequences' heads
+    const int eights = quotient(id >> 3, g.kv_heads), first = eights * 8 * a.kv_heads;
+    if (first + 8 * a.kv_heads <= static_cast<int>(g.p.suffix_wgs))
+      id = first + (id & 7) * a.kv_heads + remainder_of(id >> 3, eights, g.kv_heads);
+    const int q1 = quotient(id, g.kv_heads), q2 = quotient(q1, g.srow_tiles), b = quotient(q2, g.ssplits);
+    hk = remainder_of(id, q1, g.kv_heads);
+    rt = remainder_of(q1, q2, g.srow_tiles);
+    const int split = remainder_of(q2, b, g.ssplits);
+    const int end = a.row_start[b + 1];
+    rbase = a.row_start[b];
+    const int len = min(max(a.suffix_len[b], 0), static_cast<int>(a.max_suffix));
+    if (rbase < 0 || end > n || rbase >= end) return;
+    n = min(end - rbase, a.max_rows);
+    if (rt * 32 >= n * g.p.groups) return;
+    k0 = split * g.p.sseg;
+    k1 = min(k0 + g.p.sseg, len);
+    if (k0 >= k1) return;
+    slot = g.p.psplits + split;
+    draft0 = len - (end - rbase);
+    src.table = a.block_table + b * a.table_stride;
   }
-  id -= before;
-  const int hk = id % a.kv_heads;
-  id /= a.kv_heads;
-  const int rt = id % g.p.srow_tiles;
-  id /= g.p.srow_tiles;
-  const int split = id % g.p.ssplits, b = id / g.p.ssplits;
-  const int rows = static_cast<int>(a.rows);
-  const int start = a.row_start[b], end = a.row_start[b + 1];
-  if (start < 0 || end > rows || start >= end) return;
-  const int n = min(end - start, a.max_rows);
-  if (rt * 32 >= n * g.p.groups) return;
-  const int len = min(max(a.suffix_len[b], 0), static_cast<int>(a.max_suffix));
-  const int k0 = split * g.p.sseg, k1 = min(k0 + g.p.sseg, len);
-  if (k0 >= k1) return;
-  src.table = a.block_table + b * a.table_stride;
-  src.k = static_cast<const uint8_t*>(a.k_pages) + hk * a.page_head * 2;
-  src.v = static_cast<const uint8_t*>(a.v_pages) + hk * a.page_head * 2;
-  src.row = a.page_row * 2;
-  A::narrow(g, src, g.p.psplits + split, hk, start, n, rt * 32, k0, k1, len - (end - start), attn_lds, pages);
+  const bool pool = src.table != nullptr;
+  src.k = static_cast<const uint8_t*>(pool ? a.k_pages : a.k_prefix) + hk * (pool ? a.page_head : a.prefix_head) * 2;
+  src.v = static_cast<const uint8_t*>(pool ? a.v_pages : a.v_prefix) + hk * (pool ? a.page_head : a.prefix_head) * 2;
+  src.row = (pool ? a.page_row : a.prefix_row) * 2;
+  if (g.p.wide && prefix)
+    A::wide(g, src, slot, hk, rt, k0, k1, attn_lds, pages);
+  else
+    A::narrow(g, src, slot, hk, rbase, n, rt * 32, k0, k1, draft0, attn_lds, pages);
 }
 
-// A (row, head)'s parts joined, in the order of their slots: one wave each.
-template <bool BF, int VEC>
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) v = fmaxf(v, __shfl_xor(v, k));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
+  return v;
+}
+
+// A (row, head)'s parts joined in a fixed order: by one wave (WAVES = 1), or
+// by the four of a workgroup, a quarter of the parts each.  The first loads --
+// maxima and sums, row starts, suffix lengths -- go out together, whatever
+// they will turn out to be needed for.
+template <bool BF, int VEC, int WAVES>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnKernelArgs g) {
   const qmv_attn_args& a = g.a;
-  const int lane = __lane_id(), D = a.head_dim;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
   const int64_t all = a.rows * a.heads;
-  if (e >= all) return;
-  const int row = static_cast<int>(e / a.heads), head = static_cast<int>(e % a.heads);
+  const int64_t e = WAVES == 4 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (WAVES == 1 && e >= all) return;
+  const int row = quotient(static_cast<int>(e), g.heads), head = remainder_of(static_cast<int>(e), row, g.heads);
+  const int most = g.p.psplits + g.p.ssplits;
+  float2 ml = make_float2(kNone, 0.f);
+  if (lane < most) ml = g.pml[lane * all + e];
   // the row's sequence: the last that starts at or before it
-  int seq = -1;
-  for (int b0 = 0; b0 < a.nseq; b0 += 64) {
-    const int b = b0 + lane;
-    seq += __popcll(__ballot(b < a.nseq && a.row_start[min(b, a.nseq)] <= row));
+  int seq = -1, start = 0, end = 0, len = 0;
+  if (a.nseq < 64) {
+    const int rs = a.row_start[min(lane, a.nseq)];
+    const int sl = a.max_suffix > 0 ? a.suffix_len[min(lane, a.nseq - 1)] : 0;
+    seq = __popcll(__ballot(lane < a.nseq && rs <= row)) - 1;
+    start = __shfl(rs, max(seq, 0));
+    end = __shfl(rs, max(seq, 0) + 1);
+    len = __shfl(sl, max(seq, 0));
+  } else {
+    for (int b0 = 0; b0 < a.nseq; b0 += 64) {
+      const int b = b0 + lane;
+      seq += __popcll(__ballot(b < a.nseq && a.row_start[min(b, a.nseq)] <= row));
+    }
+    if (seq >= 0) {
+      start = a.row_start[seq];
+      end = a.row_start[seq + 1];
+      len = a.max_suffix > 0 ? a.suffix_len[seq] : 0;
+    }
   }
   int slots = g.p.psplits;
   bool past = false;
-  if (seq >= 0) {
-    const int start = a.row_start[seq], end = a.row_start[seq + 1];
-    if (start >= 0 && row >= start && row < end && end <= a.rows) {
-      past = row - start >= a.max_rows;
-      const int len = a.max_suffix > 0 ? min(max(a.suffix_len[seq], 0), static_cast<int>(a.max_suffix)) : 0;
-      if (!past && len > 0) slots += (len + g.p.sseg - 1) / g.p.sseg;
-    }
+  if (seq >= 0 && start >= 0 && row >= start && row < end && end <= a.rows) {
+    past = row - start >= a.max_rows;
+    len = min(max(len, 0), static_cast<int>(a.max_suffix));
+    if (!past && len > 0) slots += (len + g.p.sseg - 1) / g.p.sseg;
   }
-  float mx = kNone;
-  for (int s = lane; s < slots; s += 64) mx = fmaxf(mx, g.pml[s * all + e].x);
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k));
+  slots = __builtin_amdgcn_readfirstlane(slots);
+  float mx = lane < slots ? ml.x : kNone;
+  for (int s = lane + 64; s < slots; s += 64) mx = fmaxf(mx, g.pml[s * all + e].x);
+  mx = wave_max(mx);
   float acc[VEC] = {}, l = 0.f;
   const int d = lane * VEC;
+  const float* p = g.po + e * D + min(d, D - VEC);
+  for (int s0 = 0; s0 < slots; s0 += 64) {
+    if (s0) ml = g.pml[min(s0 + lane, slots - 1) * all + e];
+    const float f = s0 + lane < slots ? __builtin_amdgcn_exp2f(ml.x - mx) : 0.f;
+    l += s0 + lane < slots ? f * ml.y : 0.f;
+    const int n = min(slots - s0, 64);
+    // eight parts' loads in flight
+    constexpr int kBatch = 8;
+    for (int s = WAVES == 4 ? wave : 0; s < n; s += kBatch * WAVES) {
+      float v[kBatch][VEC];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        __builtin_memcpy(v[u], __builtin_assume_aligned(p + (s0 + min(s + u * WAVES, n - 1)) * all * D, VEC * 4),
+                         sizeof(v[u]));
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int su = s + u * WAVES;
+        if (su >= n) break;
+        const float fs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), su));
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] = fmaf(fs, v[u][k], acc[k]);
+      }
+    }
+  }
+  l = wave_sum(l);
+  if constexpr (WAVES == 4) {
+    __shared__ float part[3][64 * VEC];
+    if (wave)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) part[wave - 1][k * 64 + lane] = acc[k];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[k] += part[w][k * 64 + lane];
+  }
+  const float inv = past ? __builtin_nanf("") : l == 0.f ? 0.f : 1.f / l;
   if (d < D) {
-#pragma unroll 4
-    for (int s = 0; s < slots; ++s) {
-      const float2 ml = g.pml[s * all + e];
-      const float f = __builtin_amdgcn_exp2f(ml.x - mx);
-      const float* p = g.po + (s * all + e) * D + d;
-      l = fmaf(f, ml.y, l);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) acc[k] = fmaf(f, p[k], acc[k]);
-    }
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_row + head * a.out_head + d;
-    const float inv = past ? __builtin_nanf("") : l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[VEC / 2];
+    uint16_t w[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; k += 2) {
-      const float x = l == 0.f && !past ? 0.f : acc[k] * inv, y = l == 0.f && !past ? 0.f : acc[k + 1] * inv;
-      if (BF)
-        w[k / 2] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)) |
-                   (__builtin_bit_cast(uint16_t, static_cast<__bf16>(y)) << 16);
-      else
-        w[k / 2] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)) |
-                   (__builtin_bit_cast(uint16_t, static_cast<_Float16>(y)) << 16);
+    for (int k = 0; k < VEC; ++k) {
+      const float x = l == 0.f && !past ? 0.f : acc[k] * inv;
+      w[k] = BF ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)) : __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
     }
-    if constexpr (VEC == 2)
-      *reinterpret_cast<uint32_t*>(out) = w[0];
-    else
-      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    __builtin_memcpy(__builtin_assume_aligned(out, VEC * 2), w, sizeof(w));
   }
   if (a.lse && lane == 0)
     a.lse[e] = past ? __builtin_nanf("") : l == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(l)) * kLn2;
@@ -680,31 +779,60 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnKernelArgs g) 
 
 static int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// How many ranges to cut `keys` into for each of `units` row tiles: the fewest
+// microseconds, by what workgroups were measured to take, two a compute unit
+// at a time -- `start` to begin and end, `tile` for each `tile_keys` keys --
+// and the parts' way through the workspace, written and read at 4 TB/s.
+static int64_t key_ranges(int64_t keys, int64_t units, int tile_keys, double start, double tile, double part_bytes) {
+  constexpr int kResident = 512;
+  const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
+  double best = 1e30;
+  int64_t n = 1;
+  for (int64_t s = 1; s <= tiles && s <= 256; ++s) {
+    const double rounds = static_cast<double>((units * s + kResident - 1) / kResident);
+    const double us = rounds * (start + tile * static_cast<double>((tiles + s - 1) / s)) +
+                      static_cast<double>(s) * part_bytes * 2 / 4e6;
+    if (us < best) {
+      best = us;
+      n = s;
+    }
+  }
+  return n;
+}
+
+// Most keys of one workgroup where they lie in pages (rounded up to a
+// multiple of 128 they and a page that they begin within still fit).
+static int64_t paged_keys(const qmv_attn_args& a) {
+  return a.page_size >= 128 ? static_cast<int64_t>(a.page_size) * (kMaxPages - 2)
+                            : static_cast<int64_t>(a.page_size) * (kMaxPages - 128 / a.page_size - 1) / 128 * 128;
+}
+
 static AttnPlan plan_attn(const qmv_attn_args& a) {
-  constexpr int kSlots = 512;  // two workgroups a compute unit
   AttnPlan p = {};
   p.groups = a.heads / a.kv_heads;
   const int64_t M = a.rows * p.groups;
+  const double part = static_cast<double>(a.rows) * a.heads * a.head_dim * 4;
   p.wide = M > 64;
   p.row_tiles = ceil_div(M, p.wide ? 128 : 32);
-  const int step = p.wide ? 256 : 128;  // fewest keys of a range
   if (a.prefix_len > 0) {
     const int64_t units = static_cast<int64_t>(p.row_tiles) * a.kv_heads;
-    int64_t splits = std::min<int64_t>(ceil_div(a.prefix_len, step), std::max<int64_t>(1, kSlots / units));
-    if (a.prefix_pages) splits = std::max<int64_t>(splits, ceil_div(a.prefix_len, kMaxPagedKeys));
-    p.pseg = ceil_div(ceil_div(a.prefix_len, splits), 64) * 64;
+    int64_t n = p.wide ? key_ranges(a.prefix_len, units, 64, 4.0, 2.0, part)
+                       : key_ranges(a.prefix_len, units, 128, 4.0, 1.5, part);
+    if (a.prefix_pages) n = std::max<int64_t>(n, ceil_div(a.prefix_len, paged_keys(a)));
+    p.pseg = ceil_div(ceil_div(a.prefix_len, n), 64) * 64;
     p.psplits = ceil_div(a.prefix_len, p.pseg);
     p.prefix_wgs = units * p.psplits;
   }
   if (a.max_suffix > 0) {
-    p.srow_tiles = ceil_div(static_cast<int64_t>(std::min<int64_t>(a.max_rows, a.rows)) * p.groups, 32);
+    p.srow_tiles = ceil_div(std::min<int64_t>(a.max_rows, a.rows) * p.groups, 32);
     const int64_t units = static_cast<int64_t>(a.nseq) * a.kv_heads * p.srow_tiles;
-    int64_t splits = std::min<int64_t>(ceil_div(a.max_suffix, 128), std::max<int64_t>(1, kSlots / units));
-    splits = std::max<int64_t>(splits, ceil_div(a.max_suffix, kMaxPagedKeys));
-    p.sseg = ceil_div(ceil_div(a.max_suffix, splits), 128) * 128;
+    const int64_t n = std::max<int64_t>(key_ranges(a.max_suffix, units, 128, 4.0, 1.5, part),
+                                        ceil_div(a.max_suffix, paged_keys(a)));
+    p.sseg = ceil_div(ceil_div(a.max_suffix, n), 128) * 128;
     p.ssplits = ceil_div(a.max_suffix, p.sseg);
     p.suffix_wgs = units * p.ssplits;
   }
+  p.suffix_first = p.sseg > p.pseg;
   return p;
 }
 
@@ -724,7 +852,7 @@ size_t attn_workspace(const qmv_attn_args& a) {
 
 template <bool BF, int DP>
 static hipError_t launch_parts(const AttnKernelArgs& g, hipStream_t s) {
-  constexpr int lds = Attn<BF, DP>::kLds + kMaxPagedKeys * 4;
+  constexpr int lds = Attn<BF, DP>::kLds + kMaxPages * 4;
   const unsigned grid = static_cast<unsigned>(g.p.prefix_wgs + g.p.suffix_wgs);
   if (grid) hipLaunchKernelGGL((attn_parts_kernel<BF, DP>), dim3(grid), dim3(256), lds, s, g);
   return hipGetLastError();
@@ -737,11 +865,21 @@ static hipError_t attn_typed(const AttnKernelArgs& g, hipStream_t s) {
                        : D <= 128 ? launch_parts<BF, 128>(g, s)
                                   : launch_parts<BF, 256>(g, s);
   if (e != hipSuccess) return e;
-  const dim3 grid(ceil_div(g.a.rows * g.a.heads, 4));
-  if (D <= 128)
-    hipLaunchKernelGGL((attn_join_kernel<BF, 2>), grid, dim3(256), 0, s, g);
-  else
-    hipLaunchKernelGGL((attn_join_kernel<BF, 4>), grid, dim3(256), 0, s, g);
+  // Few rows of many parts: four waves to a row.
+  const int64_t all = g.a.rows * g.a.heads;
+  if (all <= 8192 && g.p.psplits + g.p.ssplits >= 8) {
+    const dim3 grid(static_cast<unsigned>(all));
+    if (D <= 128)
+      hipLaunchKernelGGL((attn_join_kernel<BF, 2, 4>), grid, dim3(256), 0, s, g);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<BF, 4, 4>), grid, dim3(256), 0, s, g);
+  } else {
+    const dim3 grid(ceil_div(all, 4));
+    if (D <= 128)
+      hipLaunchKernelGGL((attn_join_kernel<BF, 2, 1>), grid, dim3(256), 0, s, g);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<BF, 4, 1>), grid, dim3(256), 0, s, g);
+  }
   return hipGetLastError();
 }
 
@@ -749,6 +887,12 @@ hipError_t attn(const qmv_attn_args& a, void* ws, hipStream_t s) {
   AttnKernelArgs g;
   g.a = a;
   g.p = plan_attn(a);
+  g.groups = fast_div(g.p.groups);
+  g.pairs = fast_div(std::max<int64_t>(1, static_cast<int64_t>(a.kv_heads) * g.p.psplits));
+  g.kv_heads = fast_div(a.kv_heads);
+  g.srow_tiles = fast_div(std::max(1, g.p.srow_tiles));
+  g.ssplits = fast_div(std::max(1, g.p.ssplits));
+  g.heads = fast_div(a.heads);
   g.pml = static_cast<float2*>(ws);
   g.po = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ml_bytes(a, g.p));
   return a.dtype == QMV_BF16 ? attn_typed<true>(g, s) : attn_typed<false>(g, s);
