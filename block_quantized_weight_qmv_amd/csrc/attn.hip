@@ -109,18 +109,19 @@ __device__ __forceinline__ int swz(int row) {
 
 // 64 lanes x 16 bytes from memory to LDS at `lds` (+ 16 x lane).  The s_nop
 // covers an M0 or address written just before, which the compiler cannot see
-// being used here.
+// being used here.  LDS accesses are kept apart from copies by the waits and
+// barriers between them (wait_copies, wait_lds, lds_barrier, which no memory
+// access crosses); so that copies may run among reads of other tiles, they
+// themselves are no such border.
 __device__ __forceinline__ void copy_to_lds(const void* src, uint32_t lds) {
   __asm__ __volatile__("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off"
                        :
-                       : "v"(src), "s"(lds)
-                       : "memory");
+                       : "v"(src), "s"(lds));
 }
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
   __asm__ __volatile__("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
                        :
-                       : "v"(off), "s"(base), "s"(lds)
-                       : "memory");
+                       : "v"(off), "s"(base), "s"(lds));
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {  // all but the last N
@@ -178,6 +179,13 @@ struct RowTile {
     m = kNone;
     l = 0.f;
     c = scale * kLog2e;
+  }
+
+  // Waits for q here, before the loop over the keys: the compiler would wait
+  // inside it, for every load, the next tile's copies among them.
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) __asm__ __volatile__("" : "+v"(q[s]));
   }
 
   // Scores of NT x 32 keys.
@@ -406,6 +414,7 @@ struct Attn {
     if (tiles) copy(0);
     Tile t;
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
+    t.arrived();
 #pragma unroll 1
     for (int tile = 0; tile < tiles; ++tile) {
       wait_copies<0>();
@@ -424,15 +433,18 @@ struct Attn {
       f32x16 s[NT];
       t.template scores<NT>(kt, lane, s);
       if (left < kWideKeys || bad) {
+        // bit j: key j of the tile is seen
+        uint64_t seen = left >= 64 ? ~uint64_t{0} : (uint64_t{1} << left) - 1;
+        if (bad) {
+          const int key = min(k0 + tile * kWideKeys + lane, k1 - 1);
+          seen &= ~__ballot(pages[(key >> src.shift) - first] < 0);
+        }
+        seen >>= 4 * (lane >> 5);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int j = 32 * n + key_of(i, lane);
-            bool seen = j < left;
-            if (bad && seen) seen = pages[((k0 + tile * kWideKeys + j) >> src.shift) - first] >= 0;
-            s[n][i] = seen ? s[n][i] : -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i)
+            s[n][i] = (static_cast<uint32_t>(seen >> (32 * n)) >> (8 * (i >> 2) + (i & 3))) & 1 ? s[n][i] : -INFINITY;
       }
       t.template softmax<NT>(s);
       t.template values<NT>(kt + kTileBytes, lane, s);
@@ -474,7 +486,9 @@ struct Attn {
     }
     Tile t;
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
-    const uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
+    uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
+    t.arrived();
+    __asm__ __volatile__("" : "+v"(mask));
 #pragma unroll 1
     for (int tile = wave; tile < tiles; tile += 4) {
       const int key0 = k0 + tile * 32;
