@@ -155,8 +155,32 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
   }
 }
 
-// A wave's 32 rows against a stream of key tiles.
-template <bool BF, int DP>
+// x and y each rounded once to the type, and what the two sum to.
+template <bool BF>
+__device__ __forceinline__ uint32_t round_pair(float x, float y, float& sum) {
+  if constexpr (BF) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 h = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
+    const b2 one = {static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)};
+    sum = __builtin_amdgcn_fdot2_f32_bf16(h, one, sum, false);
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    const h2_t h = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+    const h2_t one = {static_cast<_Float16>(1.0f), static_cast<_Float16>(1.0f)};
+    sum = __builtin_amdgcn_fdot2(h, one, sum, false);
+    return __builtin_bit_cast(uint32_t, h);
+  }
+}
+
+// A wave's 32 rows against a stream of key tiles.  SPLIT: the probabilities
+// enter the second product as two values of the type (split_pair), so that an
+// output is off by little but its own rounding.  Where many rows share the
+// keys the products bound the kernel, and each probability is rounded once:
+// an output's error grows by the square root of 2 (independent roundings of
+// weights and of the output), and 64 x 8 rows on 32768 tokens take SPLITGAIN.
+// The sum takes the rounded probabilities too, so that they stay a mean's
+// weights.
+template <bool BF, int DP, bool SPLIT>
 struct RowTile {
   static constexpr int KS = DP / 16, DT = DP / 32, CPR = DP / 8, ROWB = DP * 2;
   u32x4 q[KS];
@@ -206,68 +230,101 @@ struct RowTile {
     }
   }
 
-  // Scores to unnormalized probabilities, the running maximum and sum.
+  // Whether a score passes the maximum by enough to replace it; the largest of the lane's.
   template <int NT>
-  __device__ __forceinline__ void softmax(f32x16* s) {
-    float mx = s[0][0];
+  __device__ __forceinline__ bool moves(const f32x16* s, float& mx) const {
+    mx = s[0][0];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
-    if (__any(mx * c > m + kSlack)) {
-      const float both = fmaxf(mx, __shfl_xor(mx, 32));
-      const float mn = fmaxf(m, both * c);
-      const float f = __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      l *= f;
+    return __any(mx * c > m + kSlack);
+  }
+  __device__ __forceinline__ void move(float mx) {
+    const float both = fmaxf(mx, __shfl_xor(mx, 32));
+    const float mn = fmaxf(m, both * c);
+    const float f = __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l *= f;
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[t][i] *= f;
+      for (int i = 0; i < 16; ++i) o[t][i] *= f;
+  }
+
+  // NT x 32 keys' unnormalized probabilities as the second product takes them.
+  template <int NT>
+  struct Probs {
+    u32x4 hi[2 * NT], lo[SPLIT ? 2 * NT : 1];
+  };
+
+  // Registers 2 n and 2 n + 1 of the scores, exponentiated, summed and split.
+  template <int NT>
+  __device__ __forceinline__ void exp_pair(f32x16* s, int n, Probs<NT>& p) {
+    const int t = n >> 3, i = 2 * (n & 7);
+    const float x = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -m)), y = __builtin_amdgcn_exp2f(fmaf(s[t][i + 1], c, -m));
+    s[t][i] = x;
+    s[t][i + 1] = y;
+    if constexpr (SPLIT) {
+      l += x + y;
+      uint32_t hi, lo;
+      split_pair<BF>(x, y, hi, lo);
+      p.hi[n >> 2][n & 3] = hi;
+      p.lo[n >> 2][n & 3] = lo;
+    } else {
+      p.hi[n >> 2][n & 3] = round_pair<BF>(x, y, l);
     }
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -m));
-        sum[i & 3] += s[t][i];
-      }
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+
+  // V^T of 16 keys (step ks of the tile) and 32 columns (dt).
+  static __device__ __forceinline__ u32x4 value_frag(const lds_u8* vt, int lane, int ks, int dt) {
+    const int h = lane >> 5, g = (lane >> 4) & 1, a = (lane >> 2) & 3, b = lane & 3;
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    // lane (h, g, a, b): key 4 h + a (and + 8), columns 32 dt + 16 g + 4 b ..
+    const int r0 = ks * 16 + 4 * h + a, ch = 4 * dt + 2 * g + (b >> 1), in = (b & 1) * 8;
+    const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + r0 * ROWB + ((ch ^ swz<DP>(r0)) << 4) + in));
+    const i16x4 v1 =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + (r0 + 8) * ROWB + ((ch ^ swz<DP>(r0 + 8)) << 4) + in));
+    const uint2 w0 = __builtin_bit_cast(uint2, v0), w1 = __builtin_bit_cast(uint2, v1);
+    return u32x4{w0.x, w0.y, w1.x, w1.y};
   }
 
   // o += V^T P^T over NT x 32 keys.
   template <int NT>
-  __device__ __forceinline__ void values(const lds_u8* vt, int lane, const f32x16* s) {
-    const int h = lane >> 5, g = (lane >> 4) & 1, a = (lane >> 2) & 3, b = lane & 3;
+  __device__ __forceinline__ void values(const lds_u8* vt, int lane, const Probs<NT>& p) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int ks = 0; ks < 2 * NT; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t x, y;
-          split_pair<BF>(s[t][8 * ks + 2 * k], s[t][8 * ks + 2 * k + 1], x, y);
-          hi[k] = x;
-          lo[k] = y;
-        }
-        // lane (h, g, a, b): key 4 h + a (and + 8), columns 32 dt + 16 g + 4 b ..
-        const int r0 = t * 32 + ks * 16 + 4 * h + a;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const int ch = 4 * dt + 2 * g + (b >> 1), in = (b & 1) * 8;
-          typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-          const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4*)(vt + r0 * ROWB + ((ch ^ swz<DP>(r0)) << 4) + in));
-          const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_i16x4*)(vt + (r0 + 8) * ROWB + ((ch ^ swz<DP>(r0 + 8)) << 4) + in));
-          const uint2 w0 = __builtin_bit_cast(uint2, v0), w1 = __builtin_bit_cast(uint2, v1);
-          const u32x4 vf = {w0.x, w0.y, w1.x, w1.y};
-          o[dt] = mfma<BF>(vf, hi, o[dt]);
-          o[dt] = mfma<BF>(vf, lo, o[dt]);
-        }
+      for (int dt = 0; dt < DT; ++dt) {
+        const u32x4 vf = value_frag(vt, lane, ks, dt);
+        o[dt] = mfma<BF>(vf, p.hi[ks], o[dt]);
+        if constexpr (SPLIT) o[dt] = mfma<BF>(vf, p.lo[ks], o[dt]);
       }
+  }
+
+  // The same for one tile, p, among the exponentials of the next, s to next:
+  // a matrix instruction takes as long as the half dozen vector instructions
+  // of a pair of scores, and the two kinds run side by side.  Reads of V lead
+  // by two fragments.
+  template <int NT>
+  __device__ __forceinline__ void values_and_exps(const lds_u8* vt, int lane, const Probs<NT>& p, f32x16* s,
+                                                  Probs<NT>& next) {
+    static_assert(!SPLIT, "");
+    constexpr int kSteps = 2 * NT * DT, kPairs = 8 * NT;
+    u32x4 vf[3];
+    vf[0] = value_frag(vt, lane, 0, 0);
+    vf[1] = value_frag(vt, lane, 1 / DT, 1 % DT);
+#pragma unroll
+    for (int n = 0; n < kSteps; ++n) {
+      const int ks = n / DT, dt = n % DT;
+      if (n + 2 < kSteps) vf[(n + 2) % 3] = value_frag(vt, lane, (n + 2) / DT, (n + 2) % DT);
+      o[dt] = mfma<BF>(vf[n % 3], p.hi[ks], o[dt]);
+#pragma unroll
+      for (int k = n * kPairs / kSteps; k < (n + 1) * kPairs / kSteps; ++k) exp_pair<NT>(s, k, next);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+      __builtin_amdgcn_sched_group_barrier(0x002, 6 * kPairs / kSteps, 0);  // vector
+    }
   }
 };
 
@@ -350,7 +407,8 @@ __device__ __forceinline__ int key_of(int i, int lane) { return 8 * (i >> 2) + 4
 
 template <bool BF, int DP>
 struct Attn {
-  typedef RowTile<BF, DP> Tile;
+  typedef RowTile<BF, DP, false> WideTile;
+  typedef RowTile<BF, DP, true> NarrowTile;
 
   // Whether a copy instruction's rows have one base address and 32-bit offsets.
   static __device__ __forceinline__ bool copies_by_instruction(const KeySource& src, bool bad) {
@@ -369,10 +427,10 @@ struct Attn {
   }
 
   // The unnormalized output of a lane's row to the workspace (wide).
-  static __device__ __forceinline__ void store(const Tile& t, float* po, float2* pml, int D, int lane) {
+  static __device__ __forceinline__ void store(const WideTile& t, float* po, float2* pml, int D, int lane) {
     const float l = t.l + __shfl_xor(t.l, 32);
 #pragma unroll
-    for (int dt = 0; dt < Tile::DT; ++dt)
+    for (int dt = 0; dt < WideTile::DT; ++dt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int d = 32 * dt + 8 * i + 4 * (lane >> 5);
@@ -384,8 +442,7 @@ struct Attn {
   }
 
   // 128 rows (32 a wave) against keys [k0, k1) of the prefix; the four waves
-  // share each tile, double-buffered: one barrier a tile, and a tile's copies
-  // run while the one before it is multiplied.
+  // share each tile, K and V double-buffered, with one barrier a tile.
   static __device__ __forceinline__ void wide(const AttnKernelArgs& g, const KeySource& src, int slot, int hk, int rt,
                                               int k0, int k1, uint8_t* smem, int* pages) {
     const qmv_attn_args& a = g.a;
@@ -397,57 +454,96 @@ struct Attn {
     if (src.table) bad = load_pages(src, k0, k1, pages);
     const int first = src.table ? k0 >> src.shift : 0;
     const int* pg = src.table ? pages : nullptr;
-    constexpr int NI = kWideKeys / 4 / RPI;
+    constexpr int NI = kWideKeys / 4 / RPI, NT = kWideKeys / 32;
     const int row0 = wave * (kWideKeys / 4);
     TileCopy<DP, NI> cp;
     cp.init(src, lane, D);
     const bool each = copies_by_instruction(src, bad);
     const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)smem));
     const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + kWideKeys - 1) / kWideKeys;
-    constexpr int NT = kWideKeys / 32;
-    auto copy = [&](int tile) {
-      const int key0 = k0 + tile * kWideKeys;
-      const uint32_t at = lds + (tile & 1) * 2 * kTileBytes;
-      cp.copy(src, src.k, pg, first, each, key0, k1, row0, at, lane, D);
-      cp.copy(src, src.v, pg, first, each, key0, k1, row0, at + kTileBytes, lane, D);
+    // K of tile i in buffer i & 1, V in the two after them
+    auto copy_k = [&](int tile) {
+      cp.copy(src, src.k, pg, first, each, k0 + tile * kWideKeys, k1, row0, lds + (tile & 1) * kTileBytes, lane, D);
     };
-    if (tiles) copy(0);
-    Tile t;
+    auto copy_v = [&](int tile) {
+      cp.copy(src, src.v, pg, first, each, k0 + tile * kWideKeys, k1, row0, lds + (2 + (tile & 1)) * kTileBytes, lane, D);
+    };
+    auto partial = [&](int tile) { return bad || k1 - k0 - tile * kWideKeys < kWideKeys; };
+    auto hide = [&](int tile, f32x16* s) {
+      if (!partial(tile)) return;
+      // bit j: key j of the tile is seen
+      const int left = k1 - k0 - tile * kWideKeys;
+      uint64_t seen = left >= 64 ? ~uint64_t{0} : (uint64_t{1} << left) - 1;
+      if (bad) {
+        const int key = min(k0 + tile * kWideKeys + lane, k1 - 1);
+        seen &= ~__ballot(pages[(key >> src.shift) - first] < 0);
+      }
+      seen >>= 4 * (lane >> 5);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[n][i] = (static_cast<uint32_t>(seen >> (32 * n)) >> (8 * (i >> 2) + (i & 3))) & 1 ? s[n][i] : -INFINITY;
+    };
+    // (values of keys that are not there: 0 x infinity or NaN is not 0)
+    auto clear = [&](int tile) {
+      if (!partial(tile)) return;
+      const int left = k1 - k0 - tile * kWideKeys;
+      for (int r = threadIdx.x / CPR; r < kWideKeys; r += 256 / CPR)
+        if (r >= left || (bad && pages[((k0 + tile * kWideKeys + r) >> src.shift) - first] < 0))
+          zero_chunk((lds_u8*)smem + (2 + (tile & 1)) * kTileBytes + r * ROWB + threadIdx.x % CPR * 16);
+      lds_barrier();
+    };
+    WideTile t;
+    typename WideTile::template Probs<NT> p;
+    f32x16 s[NT];
+    float mx;
+    const lds_u8* lk = (const lds_u8*)smem;
+    const bool active = m0 < M;  // (other waves only copy)
+    if (tiles) copy_k(0);
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     t.arrived();
+    wait_copies<0>();
+    lds_barrier();
+    if (tiles) {
+      copy_v(0);
+      if (tiles > 1) copy_k(1);
+      if (active) {
+        t.template scores<NT>(lk, lane, s);
+        hide(0, s);
+        if (t.template moves<NT>(s, mx)) t.move(mx);
+#pragma unroll
+        for (int n = 0; n < 8 * NT; ++n) t.template exp_pair<NT>(s, n, p);
+      }
+    }
+    // Tile i's second product runs beside tile i + 1's first and its
+    // exponentials; the copies of K two tiles and V one tile ahead run under both.
 #pragma unroll 1
-    for (int tile = 0; tile < tiles; ++tile) {
+    for (int tile = 0; tile + 1 < tiles; ++tile) {
       wait_copies<0>();
       lds_barrier();
-      if (tile + 1 < tiles) copy(tile + 1);
-      lds_u8* kt = (lds_u8*)smem + (tile & 1) * 2 * kTileBytes;
-      const int left = k1 - k0 - tile * kWideKeys;
-      if (left < kWideKeys || bad) {
-        // values of keys that are not there: 0 x infinity or NaN is not 0
-        for (int r = threadIdx.x / CPR; r < kWideKeys; r += 256 / CPR)
-          if (r >= left || (bad && pages[((k0 + tile * kWideKeys + r) >> src.shift) - first] < 0))
-            zero_chunk(kt + kTileBytes + r * ROWB + threadIdx.x % CPR * 16);
-        lds_barrier();
-      }
-      if (m0 >= M) continue;  // (whole waves: they only copy)
-      f32x16 s[NT];
-      t.template scores<NT>(kt, lane, s);
-      if (left < kWideKeys || bad) {
-        // bit j: key j of the tile is seen
-        uint64_t seen = left >= 64 ? ~uint64_t{0} : (uint64_t{1} << left) - 1;
-        if (bad) {
-          const int key = min(k0 + tile * kWideKeys + lane, k1 - 1);
-          seen &= ~__ballot(pages[(key >> src.shift) - first] < 0);
-        }
-        seen >>= 4 * (lane >> 5);
+      copy_v(tile + 1);
+      if (tile + 2 < tiles) copy_k(tile + 2);
+      clear(tile);
+      if (!active) continue;
+      const lds_u8* vt = lk + (2 + (tile & 1)) * kTileBytes;
+      t.template scores<NT>(lk + ((tile + 1) & 1) * kTileBytes, lane, s);
+      hide(tile + 1, s);
+      if (t.template moves<NT>(s, mx)) {
+        t.template values<NT>(vt, lane, p);  // (what p was made with the old maximum)
+        t.move(mx);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[n][i] = (static_cast<uint32_t>(seen >> (32 * n)) >> (8 * (i >> 2) + (i & 3))) & 1 ? s[n][i] : -INFINITY;
+        for (int k = 0; k < 2 * NT; ++k) p.hi[k] = u32x4{0, 0, 0, 0};
       }
-      t.template softmax<NT>(s);
-      t.template values<NT>(kt + kTileBytes, lane, s);
+      typename WideTile::template Probs<NT> next;
+      t.template values_and_exps<NT>(vt, lane, p, s, next);
+      p = next;
+    }
+    if (tiles) {
+      wait_copies<0>();
+      lds_barrier();
+      clear(tiles - 1);
+      if (active) t.template values<NT>(lk + (2 + ((tiles - 1) & 1)) * kTileBytes, lane, p);
     }
     if (m0 + (lane & 31) < M) {
       const size_t at = static_cast<size_t>(slot) * a.rows * a.heads + static_cast<size_t>(row) * a.heads + head;
@@ -484,7 +580,7 @@ struct Attn {
       cp.copy(src, src.k, pg, first, each, k0 + wave * 32, k1, 0, klds, lane, D);
       cp.copy(src, src.v, pg, first, each, k0 + wave * 32, k1, 0, vlds, lane, D);
     }
-    Tile t;
+    NarrowTile t;
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
     t.arrived();
@@ -516,10 +612,14 @@ struct Attn {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[0][i] = (seen >> (8 * (i >> 2) + (i & 3))) & 1 ? s[0][i] : -INFINITY;
       }
-      t.template softmax<1>(s);
+      float mx;
+      if (t.template moves<1>(s, mx)) t.move(mx);
+      typename NarrowTile::template Probs<1> p;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) t.template exp_pair<1>(s, n, p);
       if (more) wait_copies<NI>(); else wait_copies<0>();
       if (partly) unseen_values(t, s[0], vt, lane, bad ? 0 : min(draft0, k1) - key0, D);
-      t.template values<1>(vt, lane, s);
+      t.template values<1>(vt, lane, p);
       wait_lds();
       if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane, D);
     }
@@ -533,7 +633,7 @@ struct Attn {
       // rows are 16-byte chunks, permuted by the row against bank conflicts
       float4* p = reinterpret_cast<float4*>(parts + (wave * 32 + (lane & 31)) * DP);
 #pragma unroll
-      for (int dt = 0; dt < Tile::DT; ++dt)
+      for (int dt = 0; dt < NarrowTile::DT; ++dt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           p[(8 * dt + 2 * i + (lane >> 5)) ^ (lane & 7)] =
@@ -576,7 +676,7 @@ struct Attn {
   // end or on pages outside the pool by none), and 0 x infinity or NaN is not
   // 0: values of tile rows from `from` on that are not finite are added here
   // to the rows that see them, and zeroed for the product.
-  static __device__ __forceinline__ void unseen_values(Tile& t, const f32x16& p, lds_u8* vt, int lane, int from,
+  static __device__ __forceinline__ void unseen_values(NarrowTile& t, const f32x16& p, lds_u8* vt, int lane, int from,
                                                        int D) {
     const int r = lane & 31;
     constexpr uint16_t kExp = BF ? 0x7F80u : 0x7C00u;  // (columns past D, where D is not DP, are some of the row's)
@@ -605,7 +705,7 @@ struct Attn {
       pk = (lane >> 5) == ((kk >> 2) & 1) ? pk : other;
       const bool seen = !(pk == 0.f);
 #pragma unroll
-      for (int dt = 0; dt < Tile::DT; ++dt)
+      for (int dt = 0; dt < NarrowTile::DT; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int d = 32 * dt + key_of(i, lane);
