@@ -26,6 +26,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_util.h"
 #include "launch.h"
@@ -186,7 +187,8 @@ struct RowTile {
   u32x4 q[KS];
   f32x16 o[DT];
   float m, l;
-  float c;  // scale log2 e
+  float c;                    // scale log2 e
+  uint32_t koff[KS], voff[DT];  // this lane's place in a tile's K for step ks, in V for columns dt
 
   // qp: this lane's row (its first element); d past D counts as zero.
   __device__ __forceinline__ void init(const uint16_t* qp, int D, float scale, int lane) {
@@ -203,6 +205,15 @@ struct RowTile {
     m = kNone;
     l = 0.f;
     c = scale * kLog2e;
+    // K: key lane & 31, chunk 2 ks + lane / 32
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) koff[ks] = r * ROWB + (((2 * ks + h) ^ swz<DP>(r)) << 4);
+    // V, lane (h, g, a, b): key 4 h + a (and + 8), columns 32 dt + 16 g + 4 b ..
+    const int g = (lane >> 4) & 1, a = (lane >> 2) & 3, b = lane & 3, k = 4 * h + a;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+      voff[dt] = k * ROWB + (((4 * dt + 2 * g + (b >> 1)) ^ swz<DP>(k)) << 4) + (b & 1) * 8;
   }
 
   // Waits for q here, before the loop over the keys: the compiler would wait
@@ -212,22 +223,30 @@ struct RowTile {
     for (int s = 0; s < KS; ++s) __asm__ __volatile__("" : "+v"(q[s]));
   }
 
-  // Scores of NT x 32 keys.
-  template <int NT>
-  __device__ __forceinline__ void scores(const lds_u8* kt, int lane, f32x16* s) {
-    const int r = lane & 31, h = lane >> 5;
+  // Scores of NT x 32 keys.  Reads of K lead by four fragments; between(n) is
+  // called before matrix instruction n.
+  template <int NT, class F>
+  __device__ __forceinline__ void scores(const lds_u8* kt, f32x16* s, F&& between) {
+    constexpr int kSteps = NT * KS, kLead = kSteps < 4 ? kSteps : 4;
+    typedef const __attribute__((address_space(3))) u32x4 lds_u32x4;
+    auto frag = [&](int n) { return *reinterpret_cast<lds_u32x4*>(kt + (n % NT) * 32 * ROWB + koff[n / NT]); };
+    u32x4 kf[kSteps];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int n = 0; n < kLead; ++n) kf[n] = frag(n);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
-      const lds_u8* row = kt + (t * 32 + r) * ROWB;
-      const int z = swz<DP>(r);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const u32x4 kf = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(row + (((2 * ks + h) ^ z) << 4));
-        s[t] = mfma<BF>(kf, q[ks], s[t]);
-      }
+    for (int n = 0; n < kSteps; ++n) {
+      if (n + kLead < kSteps) kf[n + kLead] = frag(n + kLead);
+      between(n);
+      s[n % NT] = mfma<BF>(kf[n], q[n / NT], s[n % NT]);
     }
+  }
+  template <int NT>
+  __device__ __forceinline__ void scores(const lds_u8* kt, f32x16* s) {
+    scores<NT>(kt, s, [](int) {});
   }
 
   // Whether a score passes the maximum by enough to replace it; the largest of the lane's.
@@ -277,26 +296,22 @@ struct RowTile {
   }
 
   // V^T of 16 keys (step ks of the tile) and 32 columns (dt).
-  static __device__ __forceinline__ u32x4 value_frag(const lds_u8* vt, int lane, int ks, int dt) {
-    const int h = lane >> 5, g = (lane >> 4) & 1, a = (lane >> 2) & 3, b = lane & 3;
+  __device__ __forceinline__ u32x4 value_frag(const lds_u8* vt, int ks, int dt) const {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    // lane (h, g, a, b): key 4 h + a (and + 8), columns 32 dt + 16 g + 4 b ..
-    const int r0 = ks * 16 + 4 * h + a, ch = 4 * dt + 2 * g + (b >> 1), in = (b & 1) * 8;
-    const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + r0 * ROWB + ((ch ^ swz<DP>(r0)) << 4) + in));
-    const i16x4 v1 =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + (r0 + 8) * ROWB + ((ch ^ swz<DP>(r0 + 8)) << 4) + in));
-    const uint2 w0 = __builtin_bit_cast(uint2, v0), w1 = __builtin_bit_cast(uint2, v1);
+    const lds_u8* p = vt + ks * 16 * ROWB + voff[dt];
+    const uint2 w0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+    const uint2 w1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * ROWB)));
     return u32x4{w0.x, w0.y, w1.x, w1.y};
   }
 
   // o += V^T P^T over NT x 32 keys.
   template <int NT>
-  __device__ __forceinline__ void values(const lds_u8* vt, int lane, const Probs<NT>& p) {
+  __device__ __forceinline__ void values(const lds_u8* vt, const Probs<NT>& p) {
 #pragma unroll
     for (int ks = 0; ks < 2 * NT; ++ks)
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        const u32x4 vf = value_frag(vt, lane, ks, dt);
+        const u32x4 vf = value_frag(vt, ks, dt);
         o[dt] = mfma<BF>(vf, p.hi[ks], o[dt]);
         if constexpr (SPLIT) o[dt] = mfma<BF>(vf, p.lo[ks], o[dt]);
       }
@@ -305,23 +320,24 @@ struct RowTile {
   // The same for one tile, p, among the exponentials of the next, s to next:
   // a matrix instruction takes as long as the half dozen vector instructions
   // of a pair of scores, and the two kinds run side by side.  Reads of V lead
-  // by two fragments.
+  // by four fragments.
   template <int NT>
-  __device__ __forceinline__ void values_and_exps(const lds_u8* vt, int lane, const Probs<NT>& p, f32x16* s,
-                                                  Probs<NT>& next) {
+  __device__ __forceinline__ void values_and_exps(const lds_u8* vt, const Probs<NT>& p, f32x16* s, Probs<NT>& next) {
     static_assert(!SPLIT, "");
-    constexpr int kSteps = 2 * NT * DT, kPairs = 8 * NT;
-    u32x4 vf[3];
-    vf[0] = value_frag(vt, lane, 0, 0);
-    vf[1] = value_frag(vt, lane, 1 / DT, 1 % DT);
+    constexpr int kSteps = 2 * NT * DT, kPairs = 8 * NT, kLead = kSteps < 4 ? kSteps : 4;
+    u32x4 vf[kSteps];
+#pragma unroll
+    for (int n = 0; n < kLead; ++n) vf[n] = value_frag(vt, n / DT, n % DT);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kLead, 0);  // LDS reads
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
-      const int ks = n / DT, dt = n % DT;
-      if (n + 2 < kSteps) vf[(n + 2) % 3] = value_frag(vt, lane, (n + 2) / DT, (n + 2) % DT);
-      o[dt] = mfma<BF>(vf[n % 3], p.hi[ks], o[dt]);
+      if (n + kLead < kSteps) {
+        vf[n + kLead] = value_frag(vt, (n + kLead) / DT, (n + kLead) % DT);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      o[n % DT] = mfma<BF>(vf[n], p.hi[n / DT], o[n % DT]);
 #pragma unroll
       for (int k = n * kPairs / kSteps; k < (n + 1) * kPairs / kSteps; ++k) exp_pair<NT>(s, k, next);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
       __builtin_amdgcn_sched_group_barrier(0x002, 6 * kPairs / kSteps, 0);  // vector
     }
@@ -347,6 +363,25 @@ struct TileCopy {
     for (int i = 0; i < NV; ++i)
       off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + chunk(i * RPI + lane / CPR, lane, D) * 16;
   }
+  // Lane r: where tile row row0 + r begins; an instruction takes its first row's.
+  __device__ __forceinline__ static uint64_t starts(const KeySource& src, const uint8_t* base, const int* pages, int first,
+                                                    int key0, int end, int row0, int lane) {
+    const int mine = min(key0 + row0 + lane, end - 1);
+    int64_t at = mine * src.row;
+    if (pages)
+      at = max(pages[(mine >> src.shift) - first], 0) * src.page + (mine & ((1 << src.shift) - 1)) * src.row;
+    return reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(at);
+  }
+  __device__ __forceinline__ static const void* start(uint64_t from, int i) {
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(from), i * RPI);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(from >> 32), i * RPI);
+    return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
+  }
+  // Instruction i of a tile that lies before `end` (lds: the tile's row row0).
+  __device__ __forceinline__ void one(uint64_t from, int i, uint32_t lds) const {
+    copy_to_lds(start(from, i), off[i % NV], lds + i * RPI * DP * 2);
+  }
+
   // Key key0 is the tile's row 0.  Rows past the last key before `end` repeat
   // it, and keys of pages outside the pool are page 0's: what they hold is not
   // used.  each: every instruction's rows lie in one page of the pool (or
@@ -355,26 +390,17 @@ struct TileCopy {
                                        int key0, int end, int row0, uint32_t lds, int lane, int D) const {
     const int in_page = (1 << src.shift) - 1;
     if (each) {
-      // lane r: where row r begins; an instruction takes its first row's
-      const int mine = min(key0 + row0 + lane, end - 1);
-      int64_t at = mine * src.row;
-      if (pages) at = max(pages[(mine >> src.shift) - first], 0) * src.page + (mine & in_page) * src.row;
-      const uint64_t from = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(at);
-      const auto start = [&](int i) {
-        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(from), i * RPI);
-        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(from >> 32), i * RPI);
-        return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
-      };
+      const uint64_t from = starts(src, base, pages, first, key0, end, row0, lane);
       if (key0 + row0 + NI * RPI <= end) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) copy_to_lds(start(i), off[i % NV], lds + (row0 + i * RPI) * DP * 2);
+        for (int i = 0; i < NI; ++i) one(from, i, lds + row0 * DP * 2);
       } else {
 #pragma unroll 1
         for (int i = 0; i < NI; ++i) {
           const int row = row0 + i * RPI, have = max(end - 1 - (key0 + row), 0);
           const uint32_t o = static_cast<uint32_t>(min(lane / CPR, have)) * static_cast<uint32_t>(src.row) +
                              chunk(row + lane / CPR, lane, D) * 16;
-          copy_to_lds(start(i), o, lds + row * DP * 2);
+          copy_to_lds(start(from, i), o, lds + row * DP * 2);
         }
       }
       return;
@@ -509,41 +535,70 @@ struct Attn {
       copy_v(0);
       if (tiles > 1) copy_k(1);
       if (active) {
-        t.template scores<NT>(lk, lane, s);
+        t.template scores<NT>(lk, s);
         hide(0, s);
         if (t.template moves<NT>(s, mx)) t.move(mx);
 #pragma unroll
         for (int n = 0; n < 8 * NT; ++n) t.template exp_pair<NT>(s, n, p);
       }
     }
-    // Tile i's second product runs beside tile i + 1's first and its
-    // exponentials; the copies of K two tiles and V one tile ahead run under both.
-#pragma unroll 1
-    for (int tile = 0; tile + 1 < tiles; ++tile) {
+    // Tile i's second product runs beside tile i + 1's exponentials; the copies
+    // of V one tile and of K two tiles ahead are issued among tile i + 1's
+    // first product (in a row, they wait for each other).  Even and odd tiles
+    // are written out: every LDS address is then a lane's constant and an
+    // immediate.
+    typename WideTile::template Probs<NT> q;
+    auto step = [&](auto odd, int tile, auto& now, auto& next) __attribute__((always_inline)) {
+      constexpr int kOdd = decltype(odd)::value;
+      const lds_u8* kt = lk + (1 - kOdd) * kTileBytes;
+      const lds_u8* vt = lk + (2 + kOdd) * kTileBytes;
       wait_copies<0>();
       lds_barrier();
-      copy_v(tile + 1);
-      if (tile + 2 < tiles) copy_k(tile + 2);
+      const bool inner = each && k0 + (tile + 3) * kWideKeys <= k1;
+      if (!inner || !active) {
+        copy_v(tile + 1);
+        if (tile + 2 < tiles) copy_k(tile + 2);
+      }
       clear(tile);
-      if (!active) continue;
-      const lds_u8* vt = lk + (2 + (tile & 1)) * kTileBytes;
-      t.template scores<NT>(lk + ((tile + 1) & 1) * kTileBytes, lane, s);
-      hide(tile + 1, s);
+      if (!active) return;
+      if (inner) {
+        const int key0 = k0 + (tile + 1) * kWideKeys;
+        const uint64_t fv = cp.starts(src, src.v, pg, first, key0, k1, row0, lane);
+        const uint64_t fk = cp.starts(src, src.k, pg, first, key0 + kWideKeys, k1, row0, lane);
+        const uint32_t at = lds + row0 * ROWB;
+        constexpr int kEvery = NT * WideTile::KS / (2 * NI);
+        t.template scores<NT>(kt, s, [&](int n) {
+          if (n % kEvery) return;
+          const int i = n / kEvery;
+          if (i < NI) cp.one(fv, i, at + (3 - kOdd) * kTileBytes);
+          else if (i < 2 * NI) cp.one(fk, i - NI, at + kOdd * kTileBytes);
+        });
+      } else {
+        t.template scores<NT>(kt, s);
+        hide(tile + 1, s);
+      }
       if (t.template moves<NT>(s, mx)) {
-        t.template values<NT>(vt, lane, p);  // (what p was made with the old maximum)
+        t.template values<NT>(vt, now);  // (what it was made with the old maximum)
         t.move(mx);
 #pragma unroll
-        for (int k = 0; k < 2 * NT; ++k) p.hi[k] = u32x4{0, 0, 0, 0};
+        for (int k = 0; k < 2 * NT; ++k) now.hi[k] = u32x4{0, 0, 0, 0};
       }
-      typename WideTile::template Probs<NT> next;
-      t.template values_and_exps<NT>(vt, lane, p, s, next);
-      p = next;
+      t.template values_and_exps<NT>(vt, now, s, next);
+    };
+#pragma unroll 1
+    for (int tile = 0; tile + 1 < tiles; tile += 2) {
+      step(std::integral_constant<int, 0>{}, tile, p, q);
+      if (tile + 2 >= tiles) {
+        p = q;
+        break;
+      }
+      step(std::integral_constant<int, 1>{}, tile + 1, q, p);
     }
     if (tiles) {
       wait_copies<0>();
       lds_barrier();
       clear(tiles - 1);
-      if (active) t.template values<NT>(lk + (2 + ((tiles - 1) & 1)) * kTileBytes, lane, p);
+      if (active) t.template values<NT>(lk + (2 + ((tiles - 1) & 1)) * kTileBytes, p);
     }
     if (m0 + (lane & 31) < M) {
       const size_t at = static_cast<size_t>(slot) * a.rows * a.heads + static_cast<size_t>(row) * a.heads + head;
@@ -591,7 +646,7 @@ struct Attn {
       const bool more = tile + 4 < tiles;
       f32x16 s[1];
       wait_copies<NI>();  // outstanding: this tile's K, its V
-      t.template scores<1>(kt, lane, s);
+      t.template scores<1>(kt, s);
       wait_lds();
       if (more) cp.copy(src, src.k, pg, first, each, key0 + 128, k1, 0, klds, lane, D);
       const bool partly = key0 + 32 > min(draft0, k1) || bad;  // some rows do not see some of the keys
@@ -619,7 +674,7 @@ struct Attn {
       for (int n = 0; n < 8; ++n) t.template exp_pair<1>(s, n, p);
       if (more) wait_copies<NI>(); else wait_copies<0>();
       if (partly) unseen_values(t, s[0], vt, lane, bad ? 0 : min(draft0, k1) - key0, D);
-      t.template values<1>(vt, lane, p);
+      t.template values<1>(vt, p);
       wait_lds();
       if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane, D);
     }
