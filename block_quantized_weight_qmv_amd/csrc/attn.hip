@@ -82,6 +82,7 @@ __device__ __forceinline__ int remainder_of(int n, int q, const FastDiv& f) { re
 
 struct AttnPlan {
   int groups;        // query heads per key head
+  int each;          // a copy instruction's rows lie in one page, at 32-bit offsets (suffix, and prefix in pages)
   int suffix_first;  // the suffixes' workgroups run longer: they are launched first
   int wide;          // prefix: 128-row tiles of four waves (else 32-row tiles, four waves along the keys)
   int row_tiles;     // prefix row tiles per key head
@@ -100,12 +101,14 @@ struct AttnKernelArgs {
   float2* pml;       // [slot][row * heads + head]: maximum (log2), sum
 };
 
-// The permutation of a tile row's 16-byte chunks.  Of the eight rows that a
-// first-product read takes at one chunk, and of the four rows x two chunks of
-// a transposing read, none share a bank.
+// The permutation of a tile row's 16-byte chunks.  LDS serves 256 bytes a
+// clock, 16 chunks of different banks: the first product reads 16 rows at one
+// chunk, the second's transposing reads four rows x four chunks, and either
+// set meets 16 different places (4.4 clocks a 16-byte read measured, against
+// 7.9 where pairs of them meet).
 template <int DP>
 __device__ __forceinline__ int swz(int row) {
-  return DP == 64 ? ((row >> 1) & 3) * 2 : (row & 7) * 2;
+  return DP == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
 }
 
 // 64 lanes x 16 bytes from memory to LDS at `lds` (+ 16 x lane).  The s_nop
@@ -188,7 +191,7 @@ struct RowTile {
   f32x16 o[DT];
   float m, l;
   float c;                    // scale log2 e
-  uint32_t koff[KS], voff[DT];  // this lane's place in a tile's K for step ks, in V for columns dt
+  uint32_t koff[KS], voff[DT][2];  // this lane's place in a tile's K for step ks, in V for columns dt
 
   // qp: this lane's row (its first element); d past D counts as zero.
   __device__ __forceinline__ void init(const uint16_t* qp, int D, float scale, int lane) {
@@ -213,7 +216,9 @@ struct RowTile {
     const int g = (lane >> 4) & 1, a = (lane >> 2) & 3, b = lane & 3, k = 4 * h + a;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
-      voff[dt] = k * ROWB + (((4 * dt + 2 * g + (b >> 1)) ^ swz<DP>(k)) << 4) + (b & 1) * 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        voff[dt][i] = (k + 8 * i) * ROWB + (((4 * dt + 2 * g + (b >> 1)) ^ swz<DP>(k + 8 * i)) << 4) + (b & 1) * 8;
   }
 
   // Waits for q here, before the loop over the keys: the compiler would wait
@@ -298,9 +303,9 @@ struct RowTile {
   // V^T of 16 keys (step ks of the tile) and 32 columns (dt).
   __device__ __forceinline__ u32x4 value_frag(const lds_u8* vt, int ks, int dt) const {
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    const lds_u8* p = vt + ks * 16 * ROWB + voff[dt];
-    const uint2 w0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
-    const uint2 w1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 8 * ROWB)));
+    const lds_u8* p = vt + ks * 16 * ROWB;
+    const uint2 w0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + voff[dt][0])));
+    const uint2 w1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + voff[dt][1])));
     return u32x4{w0.x, w0.y, w1.x, w1.y};
   }
 
@@ -321,8 +326,9 @@ struct RowTile {
   // a matrix instruction takes as long as the half dozen vector instructions
   // of a pair of scores, and the two kinds run side by side.  Reads of V lead
   // by four fragments.
-  template <int NT>
-  __device__ __forceinline__ void values_and_exps(const lds_u8* vt, const Probs<NT>& p, f32x16* s, Probs<NT>& next) {
+  template <int NT, class F>
+  __device__ __forceinline__ void values_and_exps(const lds_u8* vt, const Probs<NT>& p, f32x16* s, Probs<NT>& next,
+                                                  F&& between) {
     static_assert(!SPLIT, "");
     constexpr int kSteps = 2 * NT * DT, kPairs = 8 * NT, kLead = kSteps < 4 ? kSteps : 4;
     u32x4 vf[kSteps];
@@ -335,6 +341,7 @@ struct RowTile {
         vf[n + kLead] = value_frag(vt, (n + kLead) / DT, (n + kLead) % DT);
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
       }
+      between(n);
       o[n % DT] = mfma<BF>(vf[n], p.hi[n / DT], o[n % DT]);
 #pragma unroll
       for (int k = n * kPairs / kSteps; k < (n + 1) * kPairs / kSteps; ++k) exp_pair<NT>(s, k, next);
@@ -350,18 +357,17 @@ struct RowTile {
 template <int DP, int NI>
 struct TileCopy {
   static constexpr int CPR = DP / 8, RPI = 64 / CPR;
-  static constexpr int NV = RPI >= 8 ? 1 : 8 / RPI;  // instructions until the permutation repeats
+  static constexpr int NV = 16 / RPI;  // instructions until the permutation repeats
   uint32_t off[NV];  // this lane's bytes from the instruction's first row
 
   __device__ __forceinline__ static int chunk(int row, int lane, int D) {
     const int ch = (lane % CPR) ^ swz<DP>(row);
     return ch * 8 < D ? ch : 0;  // (columns past D: anything of the row; they meet zeros of q, or are not stored)
   }
-  // (row0 is a multiple of 8)
-  __device__ __forceinline__ void init(const KeySource& src, int lane, int D) {
+  __device__ __forceinline__ void init(const KeySource& src, int row0, int lane, int D) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + chunk(i * RPI + lane / CPR, lane, D) * 16;
+      off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + chunk(row0 + i * RPI + lane / CPR, lane, D) * 16;
   }
   // Lane r: where tile row row0 + r begins; an instruction takes its first row's.
   __device__ __forceinline__ static uint64_t starts(const KeySource& src, const uint8_t* base, const int* pages, int first,
@@ -377,9 +383,21 @@ struct TileCopy {
     const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(from >> 32), i * RPI);
     return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
   }
-  // Instruction i of a tile that lies before `end` (lds: the tile's row row0).
-  __device__ __forceinline__ void one(uint64_t from, int i, uint32_t lds) const {
-    copy_to_lds(start(from, i), off[i % NV], lds + i * RPI * DP * 2);
+  // The instructions' offsets for the tile at key0, whose rows from `end` on repeat the last key before it.
+  __device__ __forceinline__ void offsets(const KeySource& src, int key0, int end, int row0, int lane, uint32_t* o) const {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) o[i] = off[i % NV];
+    if (key0 + row0 + NI * RPI > end) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int rows = lane / CPR, have = max(end - 1 - (key0 + row0 + i * RPI), 0);
+        o[i] -= static_cast<uint32_t>(rows - min(rows, have)) * static_cast<uint32_t>(src.row);
+      }
+    }
+  }
+  // Instruction i of a tile whose row row0 is at `lds`.
+  __device__ __forceinline__ static void one(uint64_t from, uint32_t o, int i, uint32_t lds) {
+    copy_to_lds(start(from, i), o, lds + i * RPI * DP * 2);
   }
 
   // Key key0 is the tile's row 0.  Rows past the last key before `end` repeat
@@ -393,7 +411,7 @@ struct TileCopy {
       const uint64_t from = starts(src, base, pages, first, key0, end, row0, lane);
       if (key0 + row0 + NI * RPI <= end) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) one(from, i, lds + row0 * DP * 2);
+        for (int i = 0; i < NI; ++i) one(from, off[i % NV], i, lds + row0 * DP * 2);
       } else {
 #pragma unroll 1
         for (int i = 0; i < NI; ++i) {
@@ -435,12 +453,6 @@ template <bool BF, int DP>
 struct Attn {
   typedef RowTile<BF, DP, false> WideTile;
   typedef RowTile<BF, DP, true> NarrowTile;
-
-  // Whether a copy instruction's rows have one base address and 32-bit offsets.
-  static __device__ __forceinline__ bool copies_by_instruction(const KeySource& src, bool bad) {
-    return !bad && src.row < (int64_t{1} << 28) && (!src.table || (1 << src.shift) >= RPI);
-  }
-
   static constexpr int CPR = DP / 8, RPI = 64 / CPR, ROWB = DP * 2;
   static constexpr int kWideKeys = DP == 256 ? 32 : 64;        // keys of a wide tile
   static constexpr int kTileBytes = kWideKeys * ROWB;          // its K or V
@@ -483,16 +495,15 @@ struct Attn {
     constexpr int NI = kWideKeys / 4 / RPI, NT = kWideKeys / 32;
     const int row0 = wave * (kWideKeys / 4);
     TileCopy<DP, NI> cp;
-    cp.init(src, lane, D);
-    const bool each = copies_by_instruction(src, bad);
+    cp.init(src, row0, lane, D);
     const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)smem));
     const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + kWideKeys - 1) / kWideKeys;
     // K of tile i in buffer i & 1, V in the two after them
     auto copy_k = [&](int tile) {
-      cp.copy(src, src.k, pg, first, each, k0 + tile * kWideKeys, k1, row0, lds + (tile & 1) * kTileBytes, lane, D);
+      cp.copy(src, src.k, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (tile & 1) * kTileBytes, lane, D);
     };
     auto copy_v = [&](int tile) {
-      cp.copy(src, src.v, pg, first, each, k0 + tile * kWideKeys, k1, row0, lds + (2 + (tile & 1)) * kTileBytes, lane, D);
+      cp.copy(src, src.v, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (2 + (tile & 1)) * kTileBytes, lane, D);
     };
     auto partial = [&](int tile) { return bad || k1 - k0 - tile * kWideKeys < kWideKeys; };
     auto hide = [&](int tile, f32x16* s) {
@@ -525,7 +536,6 @@ struct Attn {
     f32x16 s[NT];
     float mx;
     const lds_u8* lk = (const lds_u8*)smem;
-    const bool active = m0 < M;  // (other waves only copy)
     if (tiles) copy_k(0);
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     t.arrived();
@@ -534,13 +544,11 @@ struct Attn {
     if (tiles) {
       copy_v(0);
       if (tiles > 1) copy_k(1);
-      if (active) {
-        t.template scores<NT>(lk, s);
-        hide(0, s);
-        if (t.template moves<NT>(s, mx)) t.move(mx);
+      t.template scores<NT>(lk, s);
+      hide(0, s);
+      if (t.template moves<NT>(s, mx)) t.move(mx);
 #pragma unroll
-        for (int n = 0; n < 8 * NT; ++n) t.template exp_pair<NT>(s, n, p);
-      }
+      for (int n = 0; n < 8 * NT; ++n) t.template exp_pair<NT>(s, n, p);
     }
     // Tile i's second product runs beside tile i + 1's exponentials; the copies
     // of V one tile and of K two tiles ahead are issued among tile i + 1's
@@ -554,36 +562,29 @@ struct Attn {
       const lds_u8* vt = lk + (2 + kOdd) * kTileBytes;
       wait_copies<0>();
       lds_barrier();
-      const bool inner = each && k0 + (tile + 3) * kWideKeys <= k1;
-      if (!inner || !active) {
-        copy_v(tile + 1);
-        if (tile + 2 < tiles) copy_k(tile + 2);
-      }
+      // (past the last tile the copies repeat its last key, into a buffer that nobody reads)
+      const int key0 = k0 + (tile + 1) * kWideKeys;
+      const uint64_t fv = cp.starts(src, src.v, pg, first, key0, k1, row0, lane);
+      const uint64_t fk = cp.starts(src, src.k, pg, first, key0 + kWideKeys, k1, row0, lane);
+      uint32_t ov[NI], ok[NI];
+      cp.offsets(src, key0, k1, row0, lane, ov);
+      cp.offsets(src, key0 + kWideKeys, k1, row0, lane, ok);
+      const uint32_t at = lds + row0 * ROWB;
       clear(tile);
-      if (!active) return;
-      if (inner) {
-        const int key0 = k0 + (tile + 1) * kWideKeys;
-        const uint64_t fv = cp.starts(src, src.v, pg, first, key0, k1, row0, lane);
-        const uint64_t fk = cp.starts(src, src.k, pg, first, key0 + kWideKeys, k1, row0, lane);
-        const uint32_t at = lds + row0 * ROWB;
-        constexpr int kEvery = NT * WideTile::KS / (2 * NI);
-        t.template scores<NT>(kt, s, [&](int n) {
-          if (n % kEvery) return;
-          const int i = n / kEvery;
-          if (i < NI) cp.one(fv, i, at + (3 - kOdd) * kTileBytes);
-          else if (i < 2 * NI) cp.one(fk, i - NI, at + kOdd * kTileBytes);
-        });
-      } else {
-        t.template scores<NT>(kt, s);
-        hide(tile + 1, s);
-      }
+      constexpr int kEveryK = NT * WideTile::KS / NI, kEveryV = 2 * NT * WideTile::DT / NI;
+      t.template scores<NT>(kt, s, [&](int n) {
+        if (n % kEveryK == 0) cp.one(fv, ov[n / kEveryK], n / kEveryK, at + (3 - kOdd) * kTileBytes);
+      });
+      hide(tile + 1, s);
       if (t.template moves<NT>(s, mx)) {
         t.template values<NT>(vt, now);  // (what it was made with the old maximum)
         t.move(mx);
 #pragma unroll
         for (int k = 0; k < 2 * NT; ++k) now.hi[k] = u32x4{0, 0, 0, 0};
       }
-      t.template values_and_exps<NT>(vt, now, s, next);
+      t.template values_and_exps<NT>(vt, now, s, next, [&](int n) {
+        if (n % kEveryV == 0) cp.one(fk, ok[n / kEveryV], n / kEveryV, at + kOdd * kTileBytes);
+      });
     };
 #pragma unroll 1
     for (int tile = 0; tile + 1 < tiles; tile += 2) {
@@ -598,7 +599,7 @@ struct Attn {
       wait_copies<0>();
       lds_barrier();
       clear(tiles - 1);
-      if (active) t.template values<NT>(lk + (2 + ((tiles - 1) & 1)) * kTileBytes, p);
+      t.template values<NT>(lk + (2 + ((tiles - 1) & 1)) * kTileBytes, p);
     }
     if (m0 + (lane & 31) < M) {
       const size_t at = static_cast<size_t>(slot) * a.rows * a.heads + static_cast<size_t>(row) * a.heads + head;
@@ -625,8 +626,8 @@ struct Attn {
     const int* pg = src.table ? pages : nullptr;
     constexpr int NI = 32 / RPI;
     TileCopy<DP, NI> cp;
-    cp.init(src, lane, D);
-    const bool each = copies_by_instruction(src, bad);
+    cp.init(src, 0, lane, D);
+    const bool each = src.table ? g.p.each : src.row < (int64_t{1} << 28);
     lds_u8* kt = (lds_u8*)smem + wave * 2 * kWaveBytes;
     lds_u8* vt = kt + kWaveBytes;
     const uint32_t klds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt)), vlds = klds + kWaveBytes;
@@ -981,7 +982,12 @@ static AttnPlan plan_attn(const qmv_attn_args& a) {
   p.groups = a.heads / a.kv_heads;
   const int64_t M = a.rows * p.groups;
   const double part = static_cast<double>(a.rows) * a.heads * a.head_dim * 4;
-  p.wide = M > 64;
+  // Rows of one copy instruction (TileCopy::RPI at this width).
+  const int rpi = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 4 : 2;
+  const int64_t near = int64_t{1} << 27;  // elements
+  const bool pages_fit = a.page_size >= rpi && a.page_row < near;
+  p.each = pages_fit;
+  p.wide = M > 64 && (a.prefix_pages ? pages_fit : a.prefix_row < near);
   p.row_tiles = ceil_div(M, p.wide ? 128 : 32);
   if (a.prefix_len > 0) {
     const int64_t units = static_cast<int64_t>(p.row_tiles) * a.kv_heads;
