@@ -949,18 +949,26 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnKernelArgs g) 
 
 static int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// Workgroups at a time: two a compute unit.
+constexpr int kResident = 512;
+// Microseconds that workgroups were measured to take beside a full chip's
+// others: to begin and end, a wide tile of 64 keys, the four waves' narrow
+// tiles of 32 (128-wide heads).
+constexpr double kStartUs = 4.0, kWideTileUs = 2.2, kNarrowTilesUs = 1.5;
+
 // How many ranges to cut `keys` into for each of `units` row tiles: the fewest
-// microseconds, by what workgroups were measured to take, two a compute unit
-// at a time -- `start` to begin and end, `tile` for each `tile_keys` keys --
-// and the parts' way through the workspace, written and read at 4 TB/s.
-static int64_t key_ranges(int64_t keys, int64_t units, int tile_keys, double start, double tile, double part_bytes) {
-  constexpr int kResident = 512;
+// microseconds, by workgroups of `tile` microseconds for each `tile_keys`
+// keys, the parts' way through the workspace, written and read at 4 TB/s, and
+// `other` microseconds of other workgroups that fill the slots left free.
+static int64_t key_ranges(int64_t keys, int64_t units, int tile_keys, double tile, double part_bytes, double other) {
   const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
   double best = 1e30;
   int64_t n = 1;
   for (int64_t s = 1; s <= tiles && s <= 256; ++s) {
-    const double rounds = static_cast<double>((units * s + kResident - 1) / kResident);
-    const double us = rounds * (start + tile * static_cast<double>((tiles + s - 1) / s)) +
+    const int64_t rounds = (units * s + kResident - 1) / kResident;
+    const double each = kStartUs + tile * static_cast<double>((tiles + s - 1) / s);
+    const double left = other - static_cast<double>(rounds * kResident - units * s) * each;
+    const double us = static_cast<double>(rounds) * each + (left > 0 ? left / kResident + kStartUs * 2 : 0.0) +
                       static_cast<double>(s) * part_bytes * 2 / 4e6;
     if (us < best) {
       best = us;
@@ -989,23 +997,27 @@ static AttnPlan plan_attn(const qmv_attn_args& a) {
   p.each = pages_fit;
   p.wide = M > 64 && (a.prefix_pages ? pages_fit : a.prefix_row < near);
   p.row_tiles = ceil_div(M, p.wide ? 128 : 32);
+  const double width = (a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256) / 128.0;
+  double suffix_us = 0.0;
+  if (a.max_suffix > 0) {
+    p.srow_tiles = ceil_div(std::min<int64_t>(a.max_rows, a.rows) * p.groups, 32);
+    // (sequences are seldom all as long as the longest: half the ranges are taken to be empty)
+    const int64_t units = static_cast<int64_t>(a.nseq) * a.kv_heads * p.srow_tiles;
+    const int64_t n = std::max<int64_t>(
+        key_ranges(a.max_suffix, (units + 1) / 2, 128, kNarrowTilesUs * width, part, 0.0), ceil_div(a.max_suffix, paged_keys(a)));
+    p.sseg = ceil_div(ceil_div(a.max_suffix, n), 128) * 128;
+    p.ssplits = ceil_div(a.max_suffix, p.sseg);
+    p.suffix_wgs = units * p.ssplits;
+    suffix_us = static_cast<double>(p.suffix_wgs) * (kStartUs + kNarrowTilesUs * width * p.sseg / 128.0);
+  }
   if (a.prefix_len > 0) {
     const int64_t units = static_cast<int64_t>(p.row_tiles) * a.kv_heads;
-    int64_t n = p.wide ? key_ranges(a.prefix_len, units, 64, 4.0, 2.0, part)
-                       : key_ranges(a.prefix_len, units, 128, 4.0, 1.5, part);
+    int64_t n = p.wide ? key_ranges(a.prefix_len, units, 64, kWideTileUs * width, part, suffix_us)
+                       : key_ranges(a.prefix_len, units, 128, kNarrowTilesUs * width, part, suffix_us);
     if (a.prefix_pages) n = std::max<int64_t>(n, ceil_div(a.prefix_len, paged_keys(a)));
     p.pseg = ceil_div(ceil_div(a.prefix_len, n), 64) * 64;
     p.psplits = ceil_div(a.prefix_len, p.pseg);
     p.prefix_wgs = units * p.psplits;
-  }
-  if (a.max_suffix > 0) {
-    p.srow_tiles = ceil_div(std::min<int64_t>(a.max_rows, a.rows) * p.groups, 32);
-    const int64_t units = static_cast<int64_t>(a.nseq) * a.kv_heads * p.srow_tiles;
-    const int64_t n = std::max<int64_t>(key_ranges(a.max_suffix, units, 128, 4.0, 1.5, part),
-                                        ceil_div(a.max_suffix, paged_keys(a)));
-    p.sseg = ceil_div(ceil_div(a.max_suffix, n), 128) * 128;
-    p.ssplits = ceil_div(a.max_suffix, p.sseg);
-    p.suffix_wgs = units * p.ssplits;
   }
   p.suffix_first = p.sseg > p.pseg;
   return p;
