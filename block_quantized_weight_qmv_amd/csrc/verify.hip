@@ -2,8 +2,8 @@
 //   p = softmax(logits / T); draft x accepted where u q(x) < p(x); the first
 //   row that is not accepted draws from max(p - q, 0), all accepted from p.
 //
-// Two launches.  The first cuts every row of logits into slices of
-// kSlice and leaves each slice's maximum, its first place and the sum of
+// Two launches.  The first cuts every row of logits into pieces of kPiece and
+// leaves each piece's maximum, its first place and the sum of
 // e^((l - maximum) / T).  In the second, one workgroup per sequence and slice:
 // every one of them settles, from those sums, which drafts are accepted, adds
 // up its slice of the row that draws, and the last of a sequence to finish
@@ -22,9 +22,13 @@
 
 namespace qmv {
 
-constexpr int kSlice = 8192, kThreads = 256, kPer = kSlice / kThreads;
+// The first launch: a wave's piece of a row, and its workgroup's four.
+constexpr int kRowThreads = 256, kRowPer = 16, kPiece = 64 * kRowPer;
+// The second: a workgroup's slice.
+constexpr int kThreads = 1024, kWaves = kThreads / 64, kPer = 8, kSlice = kThreads * kPer;
+static_assert(kSlice % kPiece == 0, "a slice is whole pieces");
 
-struct SliceStat {
+struct PieceStat {
   double sum;   // of e^((l - max) / T); of the infinities' ones where max is +inf
   float max;
   int best;     // the first place of max
@@ -32,39 +36,40 @@ struct SliceStat {
 
 struct VerifyArgs {
   qmv_verify_args a;
-  int slices;
-  SliceStat* stat;   // [row][slice]
+  int pieces, slices;
+  PieceStat* stat;   // [row][piece]
   double* part;      // [sequence][slice]: the drawing row's weights
   uint32_t* done;    // [sequence]: workgroups that have left their part
 };
 
-// e^x for x <= 0, within 1e-14 of itself: 2^n times the Taylor polynomial of
-// degree 11 of e^r, |r| <= ln 2 / 2 (its next term is 7e-15).
-__device__ __forceinline__ double exp_neg(double x) {
-  x = fmax(x, -800.0);  // (e^-800 is 0; -inf and NaN too)
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = fma(n, -0.693147180369123816, x);  // ln 2 in two parts, the first with trailing zeros
-  r = fma(n, -1.90821492927058770e-10, r);
-  double p = 1.0 / 39916800;
-  p = fma(p, r, 1.0 / 3628800);
-  p = fma(p, r, 1.0 / 362880);
-  p = fma(p, r, 1.0 / 40320);
-  p = fma(p, r, 1.0 / 5040);
-  p = fma(p, r, 1.0 / 720);
-  p = fma(p, r, 1.0 / 120);
-  p = fma(p, r, 1.0 / 24);
-  p = fma(p, r, 1.0 / 6);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
+constexpr double kLog2e = 1.4426950408889634074;
+
+// 2^y for y <= 0, within 3e-13 of itself: 2^n times the Taylor polynomial of
+// degree 10 of e^(f ln 2), |f| <= 1/2 (its next term is 2e-13).
+__device__ __forceinline__ double exp2_neg(double y) {
+  y = fmax(y, -1100.0);  // (2^-1100 is 0; -inf too)
+  const double n = __builtin_rint(y), f = y - n;
+  constexpr double k = 0.69314718055994530942;  // ln 2
+  constexpr double k2 = k * k, k3 = k2 * k, k4 = k2 * k2, k5 = k4 * k, k6 = k3 * k3;
+  double p = k5 * k5 / 3628800;
+  p = fma(p, f, k5 * k4 / 362880);
+  p = fma(p, f, k4 * k4 / 40320);
+  p = fma(p, f, k4 * k3 / 5040);
+  p = fma(p, f, k6 / 720);
+  p = fma(p, f, k5 / 120);
+  p = fma(p, f, k4 / 24);
+  p = fma(p, f, k3 / 6);
+  p = fma(p, f, k2 / 2);
+  p = fma(p, f, k);
+  p = fma(p, f, 1.0);
   return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
 }
 
 // e^((l - m) / T), the weight of a logit against the maximum m; a maximum of
-// +inf shares everything among the infinities.
-__device__ __forceinline__ double weight(float l, float m, double inv_t) {
+// +inf shares everything among the infinities.  c = log2(e) / T.
+__device__ __forceinline__ double weight(float l, float m, double c) {
   if (m == INFINITY) return l == INFINITY ? 1.0 : 0.0;
-  return exp_neg((static_cast<double>(l) - static_cast<double>(m)) * inv_t);
+  return exp2_neg((static_cast<double>(l) - static_cast<double>(m)) * c);
 }
 
 template <int DT>
@@ -119,17 +124,17 @@ __device__ __forceinline__ void load_row(const void* row, int64_t i0, int64_t n,
   }
 }
 
-// The place of value j of thread t in a slice read 16 bytes a thread at a time.
-template <int DT>
+// The place of value j of thread t of THREADS, 16 bytes a thread at a time.
+template <int DT, int THREADS>
 __device__ __forceinline__ int place(int t, int j) {
   constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
-  return (j / kV) * kThreads * kV + t * kV + j % kV;
+  return (j / kV) * THREADS * kV + t * kV + j % kV;
 }
-template <int DT>
-__device__ __forceinline__ void load_slice(const void* row, int64_t s0, int64_t n, float past, float* v) {
+template <int DT, int THREADS, int N>
+__device__ __forceinline__ void load_pieces(const void* row, int64_t s0, int t, int64_t n, float past, float* v) {
   constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
 #pragma unroll
-  for (int k = 0; k < kPer; k += kV) load_row<DT, kV>(row, s0 + place<DT>(threadIdx.x, k), n, past, v + k);
+  for (int k = 0; k < N; k += kV) load_row<DT, kV>(row, s0 + place<DT, THREADS>(t, k), n, past, v + k);
 }
 
 template <class T, class F>
@@ -145,8 +150,9 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   v = wave_fold(v, add);
   if (__lane_id() == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-  __syncthreads();
+  v = lds[0];
+#pragma unroll
+  for (int k = 1; k < kWaves; ++k) v += lds[k];
   return v;
 }
 
@@ -166,70 +172,73 @@ __device__ __forceinline__ float temperature_of(const qmv_verify_args& a, int se
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyArgs g) {
+__global__ void __launch_bounds__(kRowThreads) verify_rows_kernel(const VerifyArgs g) {
   const qmv_verify_args& a = g.a;
-  const int row = blockIdx.y, slice = blockIdx.x, tid = threadIdx.x;
-  const int64_t s0 = static_cast<int64_t>(slice) * kSlice;
-  if (slice == 0 && row == 0)
-    for (int b = tid; b < a.nseq; b += kThreads) g.done[b] = 0;
-  if (row >= a.rows) return;  // (a launch without rows only clears the counts)
-  float v[kPer];
-  load_slice<DT>(static_cast<const typename Logits<DT>::word*>(a.logits) + row * a.logits_row, s0, a.vocab, -INFINITY, v);
+  const int row = blockIdx.y, lane = __lane_id();
+  const int piece = blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.x == 0 && row == 0)
+    for (int b = threadIdx.x; b < a.nseq; b += kRowThreads) g.done[b] = 0;
+  if (row >= a.rows || piece >= g.pieces) return;  // (a launch without rows only clears the counts)
+  const int64_t s0 = static_cast<int64_t>(piece) * kPiece;
+  float v[kRowPer];
+  load_pieces<DT, 64, kRowPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + row * a.logits_row, s0, lane,
+                               a.vocab, -INFINITY, v);
   const int seq = sequence_of(a, row);
   if (seq < 0) {
-    if (slice == 0 && tid == 0) a.out_tokens[row] = -1;
+    if (piece == 0 && lane == 0) a.out_tokens[row] = -1;
     return;
   }
   const float t = temperature_of(a, seq);
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) m = fmaxf(m, v[j]);  // (NaN stays out)
-  __shared__ float mx[4];
-  __shared__ int ix[4];
-  __shared__ double sums[4];
+  for (int j = 0; j < kRowPer; ++j) m = fmaxf(m, v[j]);  // (NaN stays out)
   m = wave_fold(m, [](float x, float y) { return fmaxf(x, y); });
-  if (__lane_id() == 0) mx[tid >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   int best = INT32_MAX;
 #pragma unroll
-  for (int j = kPer - 1; j >= 0; --j) best = v[j] == m ? place<DT>(tid, j) : best;
+  for (int j = kRowPer - 1; j >= 0; --j) best = v[j] == m ? place<DT, 64>(lane, j) : best;
   best = wave_fold(best, [](int x, int y) { return min(x, y); });
-  if (__lane_id() == 0) ix[tid >> 6] = best;
   double s = 0.0;
   if (t > 0.f && m > -INFINITY) {
-    const double inv_t = 1.0 / static_cast<double>(t);
+    const double c_t = kLog2e / static_cast<double>(t);
     double s2[2] = {0.0, 0.0};
-#pragma unroll 4
-    for (int j = 0; j < kPer; ++j) s2[j & 1] += weight(fmaxf(v[j], -INFINITY), m, inv_t);
-    s = s2[0] + s2[1];
+#pragma unroll
+    for (int j = 0; j < kRowPer; ++j) s2[j & 1] += weight(fmaxf(v[j], -INFINITY), m, c_t);
+    s = wave_fold(s2[0] + s2[1], add);
   }
-  s = block_sum(s, sums);
-  if (tid == 0)
-    g.stat[static_cast<int64_t>(row) * g.slices + slice] =
-        SliceStat{s, m, static_cast<int>(s0) + min(min(ix[0], ix[1]), min(ix[2], ix[3]))};
+  if (lane == 0) g.stat[static_cast<int64_t>(row) * g.pieces + piece] = PieceStat{s, m, static_cast<int>(s0) + best};
 }
 
-// A row's maximum, its first place and its sum, from its slices' (by a wave).
+// A row's maximum, its first place and its sum, from its pieces' (by a wave).
 struct RowStat {
   float max;
   int best;
   double sum;
 };
-__device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double inv_t) {
-  const SliceStat* st = g.stat + static_cast<int64_t>(row) * g.slices;
+__device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double c_t) {
+  const PieceStat* st = g.stat + static_cast<int64_t>(row) * g.pieces;
   const int lane = __lane_id();
+  // (the first pieces are kept, 192 of them: 196608 tokens)
+  constexpr int kKeep = 3;
+  PieceStat x[kKeep];
   float m = -INFINITY;
-  for (int s = lane; s < g.slices; s += 64) m = fmaxf(m, st[s].max);
-  m = wave_fold(m, [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    x[k] = st[min(lane + 64 * k, g.pieces - 1)];
+    if (lane + 64 * k >= g.pieces) x[k] = PieceStat{0.0, -INFINITY, INT32_MAX};
+    m = fmaxf(m, x[k].max);
+  }
+  for (int s = lane + 64 * kKeep; s < g.pieces; s += 64) m = fmaxf(m, st[s].max);
+  m = wave_fold(m, [](float y, float z) { return fmaxf(y, z); });
   int best = INT32_MAX;
   double sum = 0.0;
-  for (int s = lane; s < g.slices; s += 64) {
-    const SliceStat x = st[s];
-    if (x.max == m) best = min(best, x.best);
-    sum += x.sum * weight(x.max, m, inv_t);
-  }
-  best = wave_fold(best, [](int x, int y) { return min(x, y); });
+  auto take = [&](const PieceStat& y) {
+    if (y.max == m) best = min(best, y.best);
+    sum += y.sum * weight(y.max, m, c_t);
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) take(x[k]);
+  for (int s = lane + 64 * kKeep; s < g.pieces; s += 64) take(st[s]);
+  best = wave_fold(best, [](int y, int z) { return min(y, z); });
   return RowStat{m, best, wave_fold(sum, add)};
 }
 
@@ -238,12 +247,12 @@ __device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double
 struct Draw {
   int64_t row;
   float max;
-  double sum, inv_t;
+  double sum, c_t;
   const float* q;  // NULL: one at `hot` (-1: nothing)
   int hot;
 };
 __device__ __forceinline__ double draw_weight(const Draw& d, float l, float q, int64_t i) {
-  const double w = weight(l, d.max, d.inv_t);
+  const double w = weight(l, d.max, d.c_t);
   const double take = d.q ? (q > 0.f ? static_cast<double>(q) * d.sum : 0.0) : i == d.hot ? d.sum : 0.0;
   return w > take ? w - take : 0.0;
 }
@@ -259,14 +268,14 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
 }
 
 // The token: the first whose running sum passes u times the total (by the
-// whole workgroup).  plain: p itself, from the slices' sums.
+// whole workgroup).  plain: p itself, from the pieces' sums.
 template <int DT>
 __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw& d0, float u) {
   const qmv_verify_args& a = g.a;
   const int tid = threadIdx.x, lane = __lane_id(), wave = tid >> 6;
   __shared__ double sh_goal;
-  __shared__ int sh_slice, sh_plain, sh_last[4];
-  __shared__ double sh_sum[4];
+  __shared__ int sh_slice, sh_plain, sh_first[kWaves], sh_last[kWaves];
+  __shared__ double sh_sum[kWaves];
   Draw d = d0;
   if (wave == 0) {
     bool plain = false;
@@ -274,8 +283,12 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     auto part = [&](int s) {
       if (s >= g.slices) return 0.0;
       if (!plain) return __hip_atomic_load(g.part + static_cast<int64_t>(b) * g.slices + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      const SliceStat st = g.stat[d.row * g.slices + s];
-      return st.sum * weight(st.max, d.max, d.inv_t);
+      double w = 0.0;
+      for (int k = s * (kSlice / kPiece); k < min((s + 1) * (kSlice / kPiece), g.pieces); ++k) {
+        const PieceStat st = g.stat[d.row * g.pieces + k];
+        w += st.sum * weight(st.max, d.max, d.c_t);
+      }
+      return w;
     };
     for (;;) {
       total = 0.0;
@@ -337,14 +350,16 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
   }
   first = wave_fold(first, [](int x, int y) { return min(x, y); });
   last = wave_fold(last, [](int x, int y) { return max(x, y); });
-  __shared__ int sh_first[4];
   if (lane == 0) {
     sh_first[wave] = first;
     sh_last[wave] = last;
   }
   __syncthreads();
-  first = min(min(sh_first[0], sh_first[1]), min(sh_first[2], sh_first[3]));
-  last = max(max(sh_last[0], sh_last[1]), max(sh_last[2], sh_last[3]));
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    first = min(first, sh_first[k]);
+    last = max(last, sh_last[k]);
+  }
   return first == INT32_MAX ? last : first;
 }
 
@@ -357,30 +372,27 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
   const int n = min(end - r0, a.max_rows);
   const float t = temperature_of(a, b), u = a.u_sample[b];
   const bool greedy = t == 0.f;
-  const double inv_t = greedy ? 0.0 : 1.0 / static_cast<double>(t);
+  const double c_t = greedy ? 0.0 : kLog2e / static_cast<double>(t);
 
-  // The first row whose draft is not accepted, four rows at a time.
-  __shared__ int sh_ok[4];
-  __shared__ RowStat sh_stat[4];
+  // The first row whose draft is not accepted, a wave to a row.
+  __shared__ int sh_ok[kWaves];
+  __shared__ RowStat sh_stat[kWaves];
   int at = 0;
   RowStat rs{-INFINITY, 0, 0.0};
-  for (int t0 = 0; t0 < n; t0 += 4) {
+  for (int t0 = 0; t0 < n; t0 += kWaves) {
     const int i = t0 + wave;
-    bool ok = false;
     if (i < n) {
       const int r = r0 + i;
-      const RowStat x = row_stat(g, r, inv_t);
-      if (i + 1 < n && x.max > -INFINITY) {
-        const int draft = a.tokens[r + 1];
-        if (draft >= 0 && draft < a.vocab) {
-          if (greedy) {
-            ok = draft == x.best;
-          } else {
-            const double q = a.draft_probs ? static_cast<double>(fmaxf(a.draft_probs[r * a.draft_row + draft], 0.f)) : 1.0;
-            ok = static_cast<double>(a.u_accept[r]) * q * x.sum < weight(logit<DT>(a, r, draft), x.max, inv_t);
-          }
-        }
-      }
+      const int draft = i + 1 < n ? a.tokens[r + 1] : -1;
+      const bool known = draft >= 0 && draft < a.vocab;
+      const float l = known ? logit<DT>(a, r, draft) : -INFINITY;
+      const float q = known && a.draft_probs ? fmaxf(a.draft_probs[r * a.draft_row + draft], 0.f) : 1.f;
+      const float ua = a.u_accept[r];
+      const RowStat x = row_stat(g, r, c_t);
+      bool ok = known && x.max > -INFINITY;
+      if (ok)
+        ok = greedy ? draft == x.best
+                    : static_cast<double>(ua) * static_cast<double>(q) * x.sum < weight(l, x.max, c_t);
       if (__lane_id() == 0) {
         sh_ok[wave] = ok;
         sh_stat[wave] = x;
@@ -388,11 +400,11 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     }
     __syncthreads();
     int k = 0;
-    while (k < 4 && t0 + k < n && sh_ok[k]) ++k;
+    while (k < kWaves && t0 + k < n && sh_ok[k]) ++k;
     at = t0 + k;
-    if (k < 4 && at < n) rs = sh_stat[k];
+    if (k < kWaves && at < n) rs = sh_stat[k];
+    if (k < kWaves) break;
     __syncthreads();
-    if (k < 4) break;
   }
 
   // (n > 0 here has a row that draws: the last row is never accepted)
@@ -404,23 +416,25 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     d.row = r0 + at;
     d.max = rs.max;
     d.sum = rs.sum;
-    d.inv_t = inv_t;
+    d.c_t = c_t;
     d.q = rejected && a.draft_probs ? a.draft_probs + d.row * a.draft_row : nullptr;
     d.hot = rejected && !a.draft_probs ? a.tokens[d.row + 1] : -1;
-    __shared__ double sums[4];
+    __shared__ double sums[kWaves];
     const int64_t s0 = static_cast<int64_t>(slice) * kSlice;
     float v[kPer], q[kPer];
-    load_slice<DT>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, s0, a.vocab, -INFINITY, v);
+    load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, s0, tid,
+                                    a.vocab, -INFINITY, v);
     double s = 0.0;
     if (d.q) {
       // (in the places that v holds)
       constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
 #pragma unroll
-      for (int k = 0; k < kPer; k += kV) load_row<QMV_F32, kV>(d.q, s0 + place<DT>(tid, k), a.vocab, 0.f, q + k);
+      for (int k = 0; k < kPer; k += kV)
+        load_row<QMV_F32, kV>(d.q, s0 + place<DT, kThreads>(tid, k), a.vocab, 0.f, q + k);
     }
-#pragma unroll 4
+#pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int64_t i = s0 + place<DT>(tid, j);
+      const int64_t i = s0 + place<DT, kThreads>(tid, j);
       s += i < a.vocab ? draw_weight(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, i) : 0.0;
     }
     s = block_sum(s, sums);
@@ -428,7 +442,10 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     __shared__ int sh_last;
     if (tid == 0) {
       __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + slice, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      sh_last = __hip_atomic_fetch_add(g.done + b, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+      // Only the parts, which are atomics of the same scope, are passed on:
+      // they have to be done before the count, and no cache to be written back.
+      __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+      sh_last = __hip_atomic_fetch_add(g.done + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
                 static_cast<uint32_t>(g.slices);
     }
     __syncthreads();
@@ -442,18 +459,20 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     a.out_tokens[r] = r < r0 + at ? a.tokens[r + 1] : r == r0 + at ? token : -1;
 }
 
+static int pieces_of(const qmv_verify_args& a) { return static_cast<int>((a.vocab + kPiece - 1) / kPiece); }
 static int slices_of(const qmv_verify_args& a) { return static_cast<int>((a.vocab + kSlice - 1) / kSlice); }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t verify_workspace(const qmv_verify_args& a) {
-  const size_t slices = slices_of(a);
-  return up256(a.rows * slices * sizeof(SliceStat)) + up256(a.nseq * slices * sizeof(double)) + up256(a.nseq * 4);
+  return up256(a.rows * static_cast<size_t>(pieces_of(a)) * sizeof(PieceStat)) +
+         up256(a.nseq * static_cast<size_t>(slices_of(a)) * sizeof(double)) + up256(a.nseq * 4);
 }
 
 template <int DT>
 static hipError_t verify_typed(const VerifyArgs& g, hipStream_t s) {
   const unsigned rows = static_cast<unsigned>(std::max<int64_t>(1, g.a.rows));
-  hipLaunchKernelGGL(verify_rows_kernel<DT>, dim3(g.slices, rows), dim3(kThreads), 0, s, g);
+  hipLaunchKernelGGL(verify_rows_kernel<DT>, dim3((g.pieces + kRowThreads / 64 - 1) / (kRowThreads / 64), rows),
+                     dim3(kRowThreads), 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(verify_draw_kernel<DT>, dim3(g.slices, g.a.nseq), dim3(kThreads), 0, s, g);
@@ -463,10 +482,11 @@ static hipError_t verify_typed(const VerifyArgs& g, hipStream_t s) {
 hipError_t verify(const qmv_verify_args& a, void* ws, hipStream_t s) {
   VerifyArgs g;
   g.a = a;
+  g.pieces = pieces_of(a);
   g.slices = slices_of(a);
   uint8_t* p = static_cast<uint8_t*>(ws);
-  g.stat = reinterpret_cast<SliceStat*>(p);
-  p += up256(static_cast<size_t>(a.rows) * g.slices * sizeof(SliceStat));
+  g.stat = reinterpret_cast<PieceStat*>(p);
+  p += up256(static_cast<size_t>(a.rows) * g.pieces * sizeof(PieceStat));
   g.part = reinterpret_cast<double*>(p);
   p += up256(static_cast<size_t>(a.nseq) * g.slices * sizeof(double));
   g.done = reinterpret_cast<uint32_t*>(p);
