@@ -23,8 +23,9 @@
 namespace qmv {
 
 // The first launch: a wave's piece of a row, and its workgroup's four.
-constexpr int kRowThreads = 256, kRowPer = 16, kPiece = 64 * kRowPer;
-// The second: a workgroup's slice.
+constexpr int kRowThreads = 256, kRowPer = 32, kPiece = 64 * kRowPer;
+// The second: a slice, of which a workgroup takes one or, where there are
+// sequences enough to fill the chip, several.
 constexpr int kThreads = 1024, kWaves = kThreads / 64, kPer = 8, kSlice = kThreads * kPer;
 static_assert(kSlice % kPiece == 0, "a slice is whole pieces");
 
@@ -37,6 +38,7 @@ struct PieceStat {
 struct VerifyArgs {
   qmv_verify_args a;
   int pieces, slices;
+  int span;          // slices of a workgroup of the second launch
   PieceStat* stat;   // [row][piece]
   double* part;      // [sequence][slice]: the drawing row's weights
   uint32_t* done;    // [sequence]: workgroups that have left their part
@@ -48,7 +50,8 @@ constexpr double kLog2e = 1.4426950408889634074;
 // degree 10 of e^(f ln 2), |f| <= 1/2 (its next term is 2e-13).
 __device__ __forceinline__ double exp2_neg(double y) {
   y = fmax(y, -1100.0);  // (2^-1100 is 0; -inf too)
-  const double n = __builtin_rint(y), f = y - n;
+  // (adding 1.5 x 2^52 rounds to a whole number and leaves it in the low word)
+  const double big = y + 6755399441055744.0, n = big - 6755399441055744.0, f = y - n;
   constexpr double k = 0.69314718055994530942;  // ln 2
   constexpr double k2 = k * k, k3 = k2 * k, k4 = k2 * k2, k5 = k4 * k, k6 = k3 * k3;
   double p = k5 * k5 / 3628800;
@@ -62,13 +65,15 @@ __device__ __forceinline__ double exp2_neg(double y) {
   p = fma(p, f, k2 / 2);
   p = fma(p, f, k);
   p = fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+  return __builtin_amdgcn_ldexp(p, __double2loint(big));
 }
 
 // e^((l - m) / T), the weight of a logit against the maximum m; a maximum of
-// +inf shares everything among the infinities.  c = log2(e) / T.
+// +inf shares everything among the infinities.  c = log2(e) / T.  FINITE: m
+// is known to be finite, and no branch parts the exponentials of a loop.
+template <bool FINITE = false>
 __device__ __forceinline__ double weight(float l, float m, double c) {
-  if (m == INFINITY) return l == INFINITY ? 1.0 : 0.0;
+  if (!FINITE && m == INFINITY) return l == INFINITY ? 1.0 : 0.0;
   return exp2_neg((static_cast<double>(l) - static_cast<double>(m)) * c);
 }
 
@@ -153,6 +158,7 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   v = lds[0];
 #pragma unroll
   for (int k = 1; k < kWaves; ++k) v += lds[k];
+  __syncthreads();
   return v;
 }
 
@@ -201,8 +207,14 @@ __global__ void __launch_bounds__(kRowThreads) verify_rows_kernel(const VerifyAr
   if (t > 0.f && m > -INFINITY) {
     const double c_t = kLog2e / static_cast<double>(t);
     double s2[2] = {0.0, 0.0};
+    m = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(m)));
+    if (m < INFINITY) {
 #pragma unroll
-    for (int j = 0; j < kRowPer; ++j) s2[j & 1] += weight(fmaxf(v[j], -INFINITY), m, c_t);
+      for (int j = 0; j < kRowPer; ++j) s2[j & 1] += weight<true>(fmaxf(v[j], -INFINITY), m, c_t);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRowPer; ++j) s2[0] += v[j] == INFINITY ? 1.0 : 0.0;
+    }
     s = wave_fold(s2[0] + s2[1], add);
   }
   if (lane == 0) g.stat[static_cast<int64_t>(row) * g.pieces + piece] = PieceStat{s, m, static_cast<int>(s0) + best};
@@ -217,7 +229,7 @@ struct RowStat {
 __device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double c_t) {
   const PieceStat* st = g.stat + static_cast<int64_t>(row) * g.pieces;
   const int lane = __lane_id();
-  // (the first pieces are kept, 192 of them: 196608 tokens)
+  // (the first pieces are kept, 192 of them)
   constexpr int kKeep = 3;
   PieceStat x[kKeep];
   float m = -INFINITY;
@@ -251,10 +263,25 @@ struct Draw {
   const float* q;  // NULL: one at `hot` (-1: nothing)
   int hot;
 };
+template <bool FINITE>
 __device__ __forceinline__ double draw_weight(const Draw& d, float l, float q, int64_t i) {
-  const double w = weight(l, d.max, d.c_t);
+  const double w = weight<FINITE>(l, d.max, d.c_t);
   const double take = d.q ? (q > 0.f ? static_cast<double>(q) * d.sum : 0.0) : i == d.hot ? d.sum : 0.0;
   return w > take ? w - take : 0.0;
+}
+
+// The weights of kPer logits at the given places of a row of n.
+template <class F>
+__device__ __forceinline__ void draw_weights(const Draw& d, const float* v, const float* q, int64_t n, double* w, F&& at) {
+  if (d.max < INFINITY) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      w[j] = at(j) < n ? draw_weight<true>(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, at(j)) : 0.0;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      w[j] = at(j) < n ? draw_weight<false>(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, at(j)) : 0.0;
+  }
 }
 
 // Inclusive running sum over the wave's lanes.
@@ -329,11 +356,9 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
   load_row<DT, kPer>(row, i0, a.vocab, -INFINITY, v);
   if (d.q) load_row<QMV_F32, kPer>(d.q, i0, a.vocab, 0.f, q);
   double w[kPer], s = 0.0;
+  draw_weights(d, v, q, a.vocab, w, [&](int j) { return i0 + j; });
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    w[j] = i0 + j < a.vocab ? draw_weight(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, i0 + j) : 0.0;
-    s += w[j];
-  }
+  for (int j = 0; j < kPer; ++j) s += w[j];
   double c = wave_scan(s, lane);
   if (lane == 63) sh_sum[wave] = c;
   __syncthreads();
@@ -366,7 +391,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
 template <int DT>
 __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs g) {
   const qmv_verify_args& a = g.a;
-  const int slice = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int first_slice = blockIdx.x * g.span, b = blockIdx.y, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r0 = min(max(a.row_start[b], 0), static_cast<int>(a.rows));
   const int end = min(max(a.row_start[b + 1], r0), static_cast<int>(a.rows));
   const int n = min(end - r0, a.max_rows);
@@ -420,38 +445,41 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     d.q = rejected && a.draft_probs ? a.draft_probs + d.row * a.draft_row : nullptr;
     d.hot = rejected && !a.draft_probs ? a.tokens[d.row + 1] : -1;
     __shared__ double sums[kWaves];
-    const int64_t s0 = static_cast<int64_t>(slice) * kSlice;
-    float v[kPer], q[kPer];
-    load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, s0, tid,
-                                    a.vocab, -INFINITY, v);
-    double s = 0.0;
-    if (d.q) {
-      // (in the places that v holds)
-      constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+    for (int slice = first_slice; slice < min(first_slice + g.span, g.slices); ++slice) {
+      const int64_t s0 = static_cast<int64_t>(slice) * kSlice;
+      float v[kPer], q[kPer];
+      load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, s0,
+                                      tid, a.vocab, -INFINITY, v);
+      double s = 0.0;
+      if (d.q) {
+        // (in the places that v holds)
+        constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
 #pragma unroll
-      for (int k = 0; k < kPer; k += kV)
-        load_row<QMV_F32, kV>(d.q, s0 + place<DT, kThreads>(tid, k), a.vocab, 0.f, q + k);
-    }
+        for (int k = 0; k < kPer; k += kV)
+          load_row<QMV_F32, kV>(d.q, s0 + place<DT, kThreads>(tid, k), a.vocab, 0.f, q + k);
+      }
+      double w[kPer];
+      draw_weights(d, v, q, a.vocab, w, [&](int j) { return s0 + place<DT, kThreads>(tid, j); });
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t i = s0 + place<DT, kThreads>(tid, j);
-      s += i < a.vocab ? draw_weight(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, i) : 0.0;
+      for (int j = 0; j < kPer; ++j) s += w[j];
+      s = block_sum(s, sums);
+      if (tid == 0)
+        __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + slice, s, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
     }
-    s = block_sum(s, sums);
-    // The last workgroup of the sequence to leave its sum draws the token.
+    // The last workgroup of the sequence to leave its sums draws the token.
     __shared__ int sh_last;
     if (tid == 0) {
-      __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + slice, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       // Only the parts, which are atomics of the same scope, are passed on:
       // they have to be done before the count, and no cache to be written back.
       __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
       sh_last = __hip_atomic_fetch_add(g.done + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
-                static_cast<uint32_t>(g.slices);
+                gridDim.x;
     }
     __syncthreads();
     if (!sh_last) return;
     token = find_token<DT>(g, b, d, u);
-  } else if (slice != 0) {
+  } else if (first_slice != 0) {
     return;
   }
   if (tid == 0) a.accepted[b] = n > 0 ? at : 0;
@@ -475,7 +503,7 @@ static hipError_t verify_typed(const VerifyArgs& g, hipStream_t s) {
                      dim3(kRowThreads), 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(verify_draw_kernel<DT>, dim3(g.slices, g.a.nseq), dim3(kThreads), 0, s, g);
+  hipLaunchKernelGGL(verify_draw_kernel<DT>, dim3((g.slices + g.span - 1) / g.span, g.a.nseq), dim3(kThreads), 0, s, g);
   return hipGetLastError();
 }
 
@@ -484,6 +512,8 @@ hipError_t verify(const qmv_verify_args& a, void* ws, hipStream_t s) {
   g.a = a;
   g.pieces = pieces_of(a);
   g.slices = slices_of(a);
+  // about one workgroup a compute unit
+  g.span = static_cast<int>(std::min<int64_t>(g.slices, (static_cast<int64_t>(g.slices) * a.nseq + 255) / 256));
   uint8_t* p = static_cast<uint8_t*>(ws);
   g.stat = reinterpret_cast<PieceStat*>(p);
   p += up256(static_cast<size_t>(a.rows) * g.pieces * sizeof(PieceStat));
