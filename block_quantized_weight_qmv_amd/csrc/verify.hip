@@ -32,7 +32,7 @@ static_assert(kSlice % kPiece == 0, "a slice is whole pieces");
 struct PieceStat {
   double sum;   // of e^((l - max) / T); of the infinities' ones where max is +inf
   float max;
-  int best;     // the first place of max
+  int best;     // the first place of max, at temperature 0
 };
 
 struct VerifyArgs {
@@ -46,25 +46,23 @@ struct VerifyArgs {
 
 constexpr double kLog2e = 1.4426950408889634074;
 
-// 2^y for y <= 0, within 3e-13 of itself: 2^n times the Taylor polynomial of
-// degree 10 of e^(f ln 2), |f| <= 1/2 (its next term is 2e-13).
+// 2^y for y <= 0, within 3e-14 of itself: 2^n p(f), y = n + f, |f| <= 1/2, p the
+// polynomial of degree 9 that equals 2^f at the ten Chebyshev nodes of
+// [-1/2, 1/2] (1.8e-14 from it between them).
 __device__ __forceinline__ double exp2_neg(double y) {
   y = fmax(y, -1100.0);  // (2^-1100 is 0; -inf too)
   // (adding 1.5 x 2^52 rounds to a whole number and leaves it in the low word)
   const double big = y + 6755399441055744.0, n = big - 6755399441055744.0, f = y - n;
-  constexpr double k = 0.69314718055994530942;  // ln 2
-  constexpr double k2 = k * k, k3 = k2 * k, k4 = k2 * k2, k5 = k4 * k, k6 = k3 * k3;
-  double p = k5 * k5 / 3628800;
-  p = fma(p, f, k5 * k4 / 362880);
-  p = fma(p, f, k4 * k4 / 40320);
-  p = fma(p, f, k4 * k3 / 5040);
-  p = fma(p, f, k6 / 720);
-  p = fma(p, f, k5 / 120);
-  p = fma(p, f, k4 / 24);
-  p = fma(p, f, k3 / 6);
-  p = fma(p, f, k2 / 2);
-  p = fma(p, f, k);
-  p = fma(p, f, 1.0);
+  double p = 1.0205905413765595e-07;
+  p = fma(p, f, 1.3259645244887111e-06);
+  p = fma(p, f, 1.5252672924850737e-05);
+  p = fma(p, f, 0.0001540343375125101);
+  p = fma(p, f, 0.0013333558200794592);
+  p = fma(p, f, 0.0096181291939343126);
+  p = fma(p, f, 0.05550410866465167);
+  p = fma(p, f, 0.24022650695640341);
+  p = fma(p, f, 0.69314718055994617);
+  p = fma(p, f, 1.0000000000000135);
   return __builtin_amdgcn_ldexp(p, __double2loint(big));
 }
 
@@ -95,12 +93,18 @@ struct Logits<QMV_BF16> {
   static __device__ __forceinline__ float get(const uint32_t* w, int i) { return bf16_to_f32(w[i / 2] >> (i & 1) * 16 & 0xFFFF); }
 };
 
+// NaN as -inf, in one instruction (fmaxf quiets its operands first).
+__device__ __forceinline__ float no_nan(float v) {
+  __asm__("v_max_f32 %0, %1, %2" : "=v"(v) : "v"(v), "s"(-INFINITY));
+  return v;
+}
+
 // One logit, NaN as -inf.
 template <int DT>
 __device__ __forceinline__ float logit(const qmv_verify_args& a, int64_t row, int64_t i) {
   const typename Logits<DT>::word w = static_cast<const typename Logits<DT>::word*>(a.logits)[row * a.logits_row + i];
   const uint32_t v = w;
-  return fmaxf(Logits<DT>::get(&v, 0), -INFINITY);
+  return no_nan(Logits<DT>::get(&v, 0));
 }
 
 // N consecutive values from place i0 of a row of n, at any alignment of its
@@ -142,25 +146,48 @@ __device__ __forceinline__ void load_pieces(const void* row, int64_t s0, int t, 
   for (int k = 0; k < N; k += kV) load_row<DT, kV>(row, s0 + place<DT, THREADS>(t, k), n, past, v + k);
 }
 
+// v of the lane that a DPP control names (lanes without one, or outside the
+// row mask: zero).
+template <int CTRL, int ROWS = 0xF, class T>
+__device__ __forceinline__ T dpp_of(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(T, static_cast<uint64_t>(hi) << 32 | lo);
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, true));
+  }
+}
+
+// f over the wave, to every lane, in a fixed order: quads, halves of a row of
+// 16 and rows by DPP, then rows and halves of the wave by swaps.
 template <class T, class F>
 __device__ __forceinline__ T wave_fold(T v, F&& f) {
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) v = f(v, __shfl_xor(v, k));
+  v = f(v, dpp_of<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, dpp_of<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = f(v, dpp_of<0x141>(v));  // row_half_mirror
+  v = f(v, dpp_of<0x140>(v));  // row_mirror
+  auto swap16 = [](uint32_t x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); };
+  auto swap32 = [](uint32_t x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); };
+  auto both = [&](auto swap) {
+    if constexpr (sizeof(T) == 8) {
+      const uint64_t b = __builtin_bit_cast(uint64_t, v);
+      const auto lo = swap(static_cast<uint32_t>(b)), hi = swap(static_cast<uint32_t>(b >> 32));
+      return f(__builtin_bit_cast(T, static_cast<uint64_t>(hi[0]) << 32 | lo[0]),
+               __builtin_bit_cast(T, static_cast<uint64_t>(hi[1]) << 32 | lo[1]));
+    } else {
+      const auto x = swap(__builtin_bit_cast(uint32_t, v));
+      const uint32_t x0 = x[0], x1 = x[1];
+      return f(__builtin_bit_cast(T, x0), __builtin_bit_cast(T, x1));
+    }
+  };
+  v = both(swap16);
+  v = both(swap32);
   return v;
 }
 __device__ __forceinline__ double add(double x, double y) { return x + y; }
-
-// The sum of v over the workgroup, to every thread, in a fixed order.
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-  v = wave_fold(v, add);
-  if (__lane_id() == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = lds[0];
-#pragma unroll
-  for (int k = 1; k < kWaves; ++k) v += lds[k];
-  __syncthreads();
-  return v;
-}
+__device__ __forceinline__ float larger(float x, float y) { return x > y ? x : y; }
 
 // The sequence of a row (the last that starts at or before it), or -1.
 __device__ __forceinline__ int sequence_of(const qmv_verify_args& a, int row) {
@@ -194,27 +221,31 @@ __global__ void __launch_bounds__(kRowThreads) verify_rows_kernel(const VerifyAr
     if (piece == 0 && lane == 0) a.out_tokens[row] = -1;
     return;
   }
-  const float t = temperature_of(a, seq);
-  float m = -INFINITY;
+  const float t = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(temperature_of(a, seq))));
+  float m4[4];
 #pragma unroll
-  for (int j = 0; j < kRowPer; ++j) m = fmaxf(m, v[j]);  // (NaN stays out)
-  m = wave_fold(m, [](float x, float y) { return fmaxf(x, y); });
-  int best = INT32_MAX;
-#pragma unroll
-  for (int j = kRowPer - 1; j >= 0; --j) best = v[j] == m ? place<DT, 64>(lane, j) : best;
-  best = wave_fold(best, [](int x, int y) { return min(x, y); });
+  for (int j = 0; j < kRowPer; ++j) {
+    v[j] = no_nan(v[j]);
+    m4[j & 3] = j < 4 ? v[j] : larger(m4[j & 3], v[j]);
+  }
+  float m = wave_fold(larger(larger(m4[0], m4[1]), larger(m4[2], m4[3])), larger);
+  m = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(m)));
+  int best = 0;
   double s = 0.0;
-  if (t > 0.f && m > -INFINITY) {
+  if (t == 0.f) {  // only the first place of the maximum counts
+    best = INT32_MAX;
+#pragma unroll
+    for (int j = kRowPer - 1; j >= 0; --j) best = v[j] == m ? place<DT, 64>(lane, j) : best;
+    best = wave_fold(best, [](int x, int y) { return min(x, y); });
+  } else if (m == INFINITY) {
+#pragma unroll
+    for (int j = 0; j < kRowPer; ++j) s += v[j] == INFINITY ? 1.0 : 0.0;
+    s = wave_fold(s, add);
+  } else if (m > -INFINITY) {
     const double c_t = kLog2e / static_cast<double>(t);
     double s2[2] = {0.0, 0.0};
-    m = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(m)));
-    if (m < INFINITY) {
 #pragma unroll
-      for (int j = 0; j < kRowPer; ++j) s2[j & 1] += weight<true>(fmaxf(v[j], -INFINITY), m, c_t);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kRowPer; ++j) s2[0] += v[j] == INFINITY ? 1.0 : 0.0;
-    }
+    for (int j = 0; j < kRowPer; ++j) s2[j & 1] += weight<true>(v[j], m, c_t);
     s = wave_fold(s2[0] + s2[1], add);
   }
   if (lane == 0) g.stat[static_cast<int64_t>(row) * g.pieces + piece] = PieceStat{s, m, static_cast<int>(s0) + best};
@@ -237,10 +268,10 @@ __device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double
   for (int k = 0; k < kKeep; ++k) {
     x[k] = st[min(lane + 64 * k, g.pieces - 1)];
     if (lane + 64 * k >= g.pieces) x[k] = PieceStat{0.0, -INFINITY, INT32_MAX};
-    m = fmaxf(m, x[k].max);
+    m = larger(m, x[k].max);
   }
-  for (int s = lane + 64 * kKeep; s < g.pieces; s += 64) m = fmaxf(m, st[s].max);
-  m = wave_fold(m, [](float y, float z) { return fmaxf(y, z); });
+  for (int s = lane + 64 * kKeep; s < g.pieces; s += 64) m = larger(m, st[s].max);
+  m = wave_fold(m, larger);
   int best = INT32_MAX;
   double sum = 0.0;
   auto take = [&](const PieceStat& y) {
@@ -276,21 +307,22 @@ __device__ __forceinline__ void draw_weights(const Draw& d, const float* v, cons
   if (d.max < INFINITY) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      w[j] = at(j) < n ? draw_weight<true>(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, at(j)) : 0.0;
+      w[j] = at(j) < n ? draw_weight<true>(d, v[j], d.q ? q[j] : 0.f, at(j)) : 0.0;
   } else {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      w[j] = at(j) < n ? draw_weight<false>(d, fmaxf(v[j], -INFINITY), d.q ? q[j] : 0.f, at(j)) : 0.0;
+      w[j] = at(j) < n ? draw_weight<false>(d, v[j], d.q ? q[j] : 0.f, at(j)) : 0.0;
   }
 }
 
 // Inclusive running sum over the wave's lanes.
-__device__ __forceinline__ double wave_scan(double v, int lane) {
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) {
-    const double o = __shfl_up(v, k);
-    v = lane >= k ? v + o : v;
-  }
+__device__ __forceinline__ double wave_scan(double v) {
+  v += dpp_of<0x111>(v);  // row_shr:1
+  v += dpp_of<0x112>(v);
+  v += dpp_of<0x114>(v);
+  v += dpp_of<0x118>(v);
+  v += dpp_of<0x142, 0xA>(v);  // row_bcast:15, to rows 1 and 3
+  v += dpp_of<0x143, 0xC>(v);  // row_bcast:31, to rows 2 and 3
   return v;
 }
 
@@ -328,7 +360,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     int slice = -1, last = 0;
     double base = 0.0;
     for (int s0 = 0; s0 < g.slices && slice < 0; s0 += 64) {
-      const double v = part(s0 + lane), c = wave_scan(v, lane) + before;
+      const double v = part(s0 + lane), c = wave_scan(v) + before;
       const uint64_t some = __ballot(v > 0.0), over = __ballot(c > goal && v > 0.0);
       if (some) last = s0 + 63 - __builtin_clzll(some);
       if (over) {
@@ -354,12 +386,14 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
   const void* row = static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row;
   float v[kPer], q[kPer];
   load_row<DT, kPer>(row, i0, a.vocab, -INFINITY, v);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) v[j] = no_nan(v[j]);
   if (d.q) load_row<QMV_F32, kPer>(d.q, i0, a.vocab, 0.f, q);
   double w[kPer], s = 0.0;
   draw_weights(d, v, q, a.vocab, w, [&](int j) { return i0 + j; });
 #pragma unroll
   for (int j = 0; j < kPer; ++j) s += w[j];
-  double c = wave_scan(s, lane);
+  double c = wave_scan(s);
   if (lane == 63) sh_sum[wave] = c;
   __syncthreads();
   for (int k = 0; k < wave; ++k) c += sh_sum[k];
@@ -444,34 +478,50 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     d.c_t = c_t;
     d.q = rejected && a.draft_probs ? a.draft_probs + d.row * a.draft_row : nullptr;
     d.hot = rejected && !a.draft_probs ? a.tokens[d.row + 1] : -1;
-    __shared__ double sums[kWaves];
-    for (int slice = first_slice; slice < min(first_slice + g.span, g.slices); ++slice) {
-      const int64_t s0 = static_cast<int64_t>(slice) * kSlice;
-      float v[kPer], q[kPer];
-      load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, s0,
-                                      tid, a.vocab, -INFINITY, v);
-      double s = 0.0;
-      if (d.q) {
-        // (in the places that v holds)
-        constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+    // (no barrier between slices: the next one's loads run under this one's sums)
+    constexpr int kGroup = 4;
+    __shared__ double sums[kGroup][kWaves];
+    const int last_slice = min(first_slice + g.span, g.slices);
+    for (int s0 = first_slice; s0 < last_slice; s0 += kGroup) {
 #pragma unroll
-        for (int k = 0; k < kPer; k += kV)
-          load_row<QMV_F32, kV>(d.q, s0 + place<DT, kThreads>(tid, k), a.vocab, 0.f, q + k);
+      for (int k = 0; k < kGroup; ++k) {
+        if (s0 + k >= last_slice) break;
+        const int64_t i0 = static_cast<int64_t>(s0 + k) * kSlice;
+        float v[kPer], q[kPer];
+        load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, i0,
+                                        tid, a.vocab, -INFINITY, v);
+        if (d.q) {
+          // (in the places that v holds)
+          constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+#pragma unroll
+          for (int j = 0; j < kPer; j += kV)
+            load_row<QMV_F32, kV>(d.q, i0 + place<DT, kThreads>(tid, j), a.vocab, 0.f, q + j);
+        }
+        double w[kPer], s = 0.0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = no_nan(v[j]);
+        draw_weights(d, v, q, a.vocab, w, [&](int j) { return i0 + place<DT, kThreads>(tid, j); });
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) s += w[j];
+        s = wave_fold(s, add);
+        if (__lane_id() == 0) sums[k][wave] = s;
       }
-      double w[kPer];
-      draw_weights(d, v, q, a.vocab, w, [&](int j) { return s0 + place<DT, kThreads>(tid, j); });
+      __syncthreads();
+      if (tid < min(kGroup, last_slice - s0)) {
+        double s = 0.0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) s += w[j];
-      s = block_sum(s, sums);
-      if (tid == 0)
-        __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + slice, s, __ATOMIC_RELAXED,
+        for (int k = 0; k < kWaves; ++k) s += sums[tid][k];
+        __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + s0 + tid, s, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
     }
     // The last workgroup of the sequence to leave its sums draws the token.
     __shared__ int sh_last;
     if (tid == 0) {
       // Only the parts, which are atomics of the same scope, are passed on:
-      // they have to be done before the count, and no cache to be written back.
+      // they have to be done before the count (this wave stored them), and no
+      // cache to be written back.
       __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
       sh_last = __hip_atomic_fetch_add(g.done + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
                 gridDim.x;
