@@ -277,31 +277,117 @@ hipError_t dequant(const qmv_weights& W, void* out, int out_dtype, hipStream_t s
   }
 }
 
-// out[i] = scale * W[ids[i]]: one workgroup per looked-up row (grid y) and
-// 1024 columns (grid x).
+// Sixteen consecutive weights k .. k + 15 of row r (k a multiple of 16: half a
+// sub-block of 32, with one scale), by 16-byte loads.  Same arithmetic as
+// dq_quad.
+template <int FMT>
+__device__ __forceinline__ void dq_half(const uint8_t* w, uint64_t scales_offset, int cols, int r, int k, float* v) {
+  constexpr bool kQ4 = FMT == QMV_Q4_K || FMT == kQ4KPlanes, kQ5 = FMT == QMV_Q5_K || FMT == kQ5KPlanes;
+  auto byte = [](const uint4& x, int i) {
+    const uint32_t d = i < 4 ? x.x : i < 8 ? x.y : i < 12 ? x.z : x.w;
+    return d >> (8 * (i & 3)) & 255;
+  };
+  if constexpr (FMT == QMV_Q8_0) {
+    const uint8_t* b = w + (static_cast<size_t>(r) * (cols / 32) + k / 32) * 34;
+    const float d = f16_to_f32(ld_u16(b));
+    const uint4 q = ld16_any(b + 2 + k % 32);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = d * static_cast<float>(static_cast<int8_t>(byte(q, e)));
+  } else if constexpr (FMT == QMV_INT4_G128) {
+    const float s = f16_to_f32(ld_u16(w + scales_offset + (static_cast<size_t>(r) * (cols / 128) + k / 128) * 2));
+    const uint2 q = ld8_any(w + static_cast<size_t>(r) * (cols / 2) + k / 2);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int u = (e < 8 ? q.x : q.y) >> (4 * (e & 7)) & 15;
+      v[e] = s * static_cast<float>(u - 8);
+    }
+  } else {
+    const size_t blk = static_cast<size_t>(r) * (cols / 256) + k / 256;
+    const int t = k % 256, l = t & 16;
+    const uint64_t a = scales_offset;
+    if constexpr (kQ4 || kQ5) {
+      const int c = t >> 6, hh = (t >> 5) & 1, s = t >> 5;
+      constexpr bool kPlanes = FMT == kQ4KPlanes || FMT == kQ5KPlanes;
+      const uint8_t* h = kPlanes ? w + 16 * blk : w + blk * (kQ4 ? 144 : 176);
+      // codes of half l of quarter c, and (Q5_K) the high bits' half
+      constexpr int kA = kQ4 ? 1 : 3, kB = kQ4 ? 5 : 7;
+      const uint8_t* qp = kPlanes ? w + (l ? kB : kA) * a + 64 * blk + 16 * c : h + (kQ4 ? 16 : 48) + 32 * c + l;
+      const uint4 head = ld16_any(h), q = ld16_any(qp);
+      uint4 qh = make_uint4(0, 0, 0, 0);
+      if constexpr (kQ5) qh = ld16_any(kPlanes ? w + (l ? 2 : 1) * a + 16 * blk : h + 16 + l);
+      const float d = f16_to_f32(head.x & 0xFFFF), dmin = f16_to_f32(head.x >> 16);
+      // scale bytes 0 .. 11 are head.y, head.z, head.w
+      const int sh = 8 * (s & 3);
+      const uint32_t b0 = head.y >> sh & 255, b1 = head.z >> sh & 255, b2 = head.w >> sh & 255;
+      const uint32_t sc = s < 4 ? b0 & 63 : (b2 & 15) | b0 >> 6 << 4, mn = s < 4 ? b1 & 63 : b2 >> 4 | b1 >> 6 << 4;
+      const float ds = d * static_cast<float>(sc), dm = dmin * static_cast<float>(mn);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        uint32_t u = byte(q, e) >> (4 * hh) & 15;
+        if constexpr (kQ5) u |= (byte(qh, e) >> s & 1) << 4;
+        v[e] = ds * static_cast<float>(u) - dm;
+      }
+    } else {
+      constexpr bool kPlanes = FMT == kQ6KPlanes;
+      const int h = t >> 7, gq = (t >> 5) & 3, i = l >> 4, p = 2 * h + i;
+      const uint8_t* b = w + blk * 210;
+      const uint4 ql = ld16_any(kPlanes ? w + 4 * (gq & 1) * a + 64 * blk + 16 * p : b + 64 * h + 32 * (gq & 1) + l);
+      const uint4 qh = ld16_any(kPlanes ? w + 8 * a + 64 * blk + 16 * p : b + 128 + 32 * h + l);
+      const int sc = static_cast<int8_t>(ld_u8(kPlanes ? w + 12 * a + 16 * blk + t / 16 : b + 192 + t / 16));
+      const float ds = f16_to_f32(ld_u16(kPlanes ? w + 13 * a + 2 * blk : b + 208)) * static_cast<float>(sc);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t u = (byte(ql, e) >> (4 * (gq >> 1)) & 15) | (byte(qh, e) >> (2 * gq) & 3) << 4;
+        v[e] = ds * static_cast<float>(static_cast<int>(u) - 32);
+      }
+    }
+  }
+}
+
+// out[i] = scale * W[ids[i]], a thread for 16 consecutive weights: a 256-thread
+// workgroup takes a row's pieces of 4096 columns (grid y), or several narrow
+// rows.  16384 rows of 3584 Q8_0 weights to bf16 take 42 us (4.2 TB/s read and
+// written; with four weights to a thread, decoded from single bytes, 80 us),
+// one Q4_K row 2 us, which is the launch.
 template <int FMT, int OUT>
 __global__ void __launch_bounds__(256)
-embed_kernel(const uint8_t* __restrict__ w, uint64_t scales_offset, int rows, int cols, const int32_t* __restrict__ ids,
-             int64_t n, float scale, void* __restrict__ out) {
-  const int quads = cols / 4;
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; idx < n * quads;
-       idx += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t i = idx / quads;
-    const int k = static_cast<int>(idx % quads) * 4;
-    const int r = ids[i];
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r >= 0 && r < rows) dq_quad<FMT>(w, scales_offset, cols, r, k, v);
-    const size_t o = static_cast<size_t>(i) * cols + k;
+embed_kernel(const uint8_t* w, uint64_t scales_offset, int rows, int cols, const int32_t* ids, int64_t n, float scale,
+             void* out) {
+  const int chunks = cols / 16, per = chunks < 256 ? 256 / chunks : 1;  // rows of a workgroup
+  const int sub = chunks < 256 ? static_cast<int>(threadIdx.x) / chunks : 0;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * per + sub;
+  if (sub >= per || i >= n) return;
+  const int r = ids[i];
+  for (int c = chunks < 256 ? static_cast<int>(threadIdx.x) - sub * chunks : blockIdx.y * 256 + threadIdx.x; c < chunks;
+       c += gridDim.y * 256) {
+    float v[16];
+    if (r >= 0 && r < rows) {
+      dq_half<FMT>(w, scales_offset, cols, r, c * 16, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= scale;
-    if (OUT == QMV_F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+      for (int e = 0; e < 16; ++e) v[e] *= scale;
     } else {
-      uint32_t h[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = OUT == QMV_F16 ? f32_to_f16_rne(v[e]) : f32_to_bf16_rne(v[e]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) =
-          make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    }
+    const size_t o = static_cast<size_t>(i) * cols + c * 16;
+    if constexpr (OUT == QMV_F32) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + o + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else {
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (OUT == QMV_F16) {
+          h[e] = f32_to_f16_rne(v[2 * e]) | f32_to_f16_rne(v[2 * e + 1]) << 16;
+        } else {
+          typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+          h[e] = __builtin_bit_cast(uint32_t, b2{static_cast<__bf16>(v[2 * e]), static_cast<__bf16>(v[2 * e + 1])});
+        }
+      }
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o);
+      p[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      p[1] = make_uint4(h[4], h[5], h[6], h[7]);
     }
   }
 }
@@ -310,21 +396,21 @@ template <int FMT>
 static hipError_t embed_fmt(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
                             hipStream_t s) {
   const int rows = static_cast<int>(W.rows), cols = static_cast<int>(W.cols);
-  const int64_t want = (n * (cols / 4) + 255) / 256;
-  const int grid = static_cast<int>(want < 65536 ? want : 65536);
+  const int chunks = cols / 16, per = chunks < 256 ? 256 / chunks : 1, pieces = (chunks + 255) / 256;
+  const dim3 grid(static_cast<unsigned>((n + per - 1) / per), pieces < 65535 ? pieces : 65535);
   const uint8_t* w = static_cast<const uint8_t*>(W.data);
   switch (out_dtype) {
     case QMV_F32:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F32>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
-                         ids, n, scale, out);
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F32>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
+                         scale, out);
       break;
     case QMV_F16:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F16>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
-                         ids, n, scale, out);
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F16>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
+                         scale, out);
       break;
     case QMV_BF16:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_BF16>), dim3(grid), dim3(256), 0, s, w, W.scales_offset, rows, cols,
-                         ids, n, scale, out);
+      hipLaunchKernelGGL((embed_kernel<FMT, QMV_BF16>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
+                         scale, out);
       break;
     default:
       return hipErrorInvalidValue;

@@ -187,7 +187,11 @@ __device__ __forceinline__ T wave_fold(T v, F&& f) {
   return v;
 }
 __device__ __forceinline__ double add(double x, double y) { return x + y; }
-__device__ __forceinline__ float larger(float x, float y) { return x > y ? x : y; }
+// (of two numbers that are not NaN; one instruction, as no_nan)
+__device__ __forceinline__ float larger(float x, float y) {
+  __asm__("v_max_f32 %0, %1, %2" : "=v"(x) : "v"(x), "v"(y));
+  return x;
+}
 
 // The sequence of a row (the last that starts at or before it), or -1.
 __device__ __forceinline__ int sequence_of(const qmv_verify_args& a, int row) {

@@ -143,14 +143,37 @@ def _ptr(a):
     return a.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream(t) -> int:
+    """The current stream of a tensor's device as an address (torch's raw lookup where it has one: 0.2 us against 1.8)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(t.get_device())
+
+
 def _stream(stream, *tensors):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
-        if hasattr(t, "is_cuda") and t.is_cuda:
-            import torch
-            return torch.cuda.current_stream(t.device).cuda_stream
+        if getattr(t, "is_cuda", False):
+            return _current_stream(t)
     return None
+
+
+_names = {}
+
+
+def _dtype_name(t) -> str:
+    d = t.dtype
+    name = _names.get(d)
+    if name is None:
+        name = _names[d] = str(d).replace("torch.", "")
+    return name
 
 
 # Tensor dtypes accepted for each activation / output dtype code (bf16 may
@@ -176,7 +199,7 @@ def _check_dev(t, what: str, dtype_code: int | None, min_elems: int) -> None:
     if not t.is_contiguous():
         raise QmvError(-6, f"{what}: tensor is not contiguous")
     if dtype_code is not None:
-        name = str(t.dtype).replace("torch.", "")
+        name = _dtype_name(t)
         if name not in _TORCH_OK[dtype_code]:
             raise QmvError(-2, f"{what}: tensor dtype {name}, expected one of {_TORCH_OK[dtype_code]}")
         have = t.numel() * t.element_size() // _ELEM[dtype_code]
@@ -403,7 +426,7 @@ def _check_vec(t, what: str, names, n: int) -> None:
     _check_dev(t, what, None, 0)
     if isinstance(t, int):
         return
-    name = str(t.dtype).replace("torch.", "")
+    name = _dtype_name(t)
     if name not in names:
         raise QmvError(-2, f"{what}: tensor dtype {name}, expected one of {names}")
     if t.numel() < n:
@@ -416,7 +439,7 @@ def _check_view(t, what: str, name: str, ndim: int) -> None:
         raise QmvError(-1, f"{what} is None")
     if not getattr(t, "is_cuda", False):
         raise QmvError(-6, f"{what}: tensor is not on a GPU")
-    if str(t.dtype).replace("torch.", "") != name:
+    if _dtype_name(t) != name:
         raise QmvError(-2, f"{what}: tensor dtype {t.dtype}, expected {name}")
     if t.dim() != ndim:
         raise QmvError(-3, f"{what}: {t.dim()} dimensions, expected {ndim}")
