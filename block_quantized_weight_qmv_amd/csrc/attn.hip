@@ -84,7 +84,8 @@ struct AttnPlan {
   int groups;        // query heads per key head
   int each;          // a copy instruction's rows lie in one page, at 32-bit offsets (suffix, and prefix in pages)
   int suffix_first;  // the suffixes' workgroups run longer: they are launched first
-  int wide;          // prefix: 128-row tiles of four waves (else 32-row tiles, four waves along the keys)
+  int wide;          // prefix: 128-row tiles of four waves (else narrow tiles, four waves along the keys)
+  int rows;          // of a narrow tile: 16 or 32
   int row_tiles;     // prefix row tiles per key head
   int psplits, pseg; // prefix key ranges and their keys
   int srow_tiles;    // suffix row tiles per sequence and key head
@@ -351,6 +352,203 @@ struct RowTile {
   }
 };
 
+// Key j of subtile register i.
+__device__ __forceinline__ int key_of(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// Elements of V's tile row kk in LDS.
+template <bool BF, int DP>
+__device__ __forceinline__ float value_at(const lds_u8* vt, int kk, int d) {
+  const uint32_t b = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
+      vt + kk * DP * 2 + (((d >> 3) ^ swz<DP>(kk)) << 4) + (d & 7) * 2);
+  return BF ? bf16_to_f32(b) : f16_to_f32(b);
+}
+
+// The narrow workgroups' row tiles, a tile of 32 keys at a time: 32 rows ...
+template <bool BF, int DP>
+struct Narrow32 : RowTile<BF, DP, true> {
+  typedef RowTile<BF, DP, true> Base;
+  static constexpr int kRows = 32;
+  struct Keys {
+    f32x16 s[1];
+  };
+  typedef typename Base::template Probs<1> P;
+
+  __device__ __forceinline__ void keys(const lds_u8* kt, Keys& k) { this->template scores<1>(kt, k.s); }
+  // seen: bit j for key j
+  static __device__ __forceinline__ void hide(Keys& k, uint32_t seen, int lane) {
+    seen >>= 4 * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) k.s[0][i] = (seen >> (8 * (i >> 2) + (i & 3))) & 1 ? k.s[0][i] : -INFINITY;
+  }
+  __device__ __forceinline__ void exps(Keys& k, P& p) {
+    float mx;
+    if (this->template moves<1>(k.s, mx)) this->move(mx);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) this->template exp_pair<1>(k.s, n, p);
+  }
+  __device__ __forceinline__ void product(const lds_u8* vt, const P& p) { this->template values<1>(vt, p); }
+  // The lane's row's probability of key kk.
+  static __device__ __forceinline__ float prob(const Keys& k, int kk, int lane) {
+    const int ri = ((kk >> 3) << 2) | (kk & 3);
+    float pk = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pk = i == ri ? k.s[0][i] : pk;
+    const float other = __shfl_xor(pk, 32);
+    return (lane >> 5) == ((kk >> 2) & 1) ? pk : other;
+  }
+  __device__ __forceinline__ void add_value(const lds_u8* vt, int kk, float pk, int lane) {
+#pragma unroll
+    for (int dt = 0; dt < Base::DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        this->o[dt][i] = fmaf(pk, value_at<BF, DP>(vt, kk, 32 * dt + key_of(i, lane)), this->o[dt][i]);
+  }
+  __device__ __forceinline__ float total() const { return this->l + __shfl_xor(this->l, 32); }
+  // The outputs as quads of columns.
+  template <class F>
+  __device__ __forceinline__ void each_quad(int lane, F&& f) const {
+#pragma unroll
+    for (int dt = 0; dt < Base::DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f(8 * dt + 2 * i + (lane >> 5), make_float4(this->o[dt][4 * i], this->o[dt][4 * i + 1], this->o[dt][4 * i + 2],
+                                                    this->o[dt][4 * i + 3]));
+  }
+};
+
+// ... or 16, on 16x16x32 instructions, where a sequence has no more (one token
+// of a group of up to 16 heads): half the matrix work, exponentials and
+// outputs of a lane.  A lane (q, n) of the products holds row n and, in the
+// first, keys 16 t + 4 q + r; one second product then spans the 32 keys, its
+// k index 8 q + j over keys 4 q + j and 16 + 4 q + j - 4.
+template <bool BF, int DP>
+struct Narrow16 {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  static constexpr int kRows = 16, KS = DP / 32, DT = DP / 16, ROWB = DP * 2;
+  struct Keys {
+    f32x4 s[2];
+  };
+  struct P {
+    u32x4 hi, lo;
+  };
+  u32x4 q[KS];
+  f32x4 o[DT];
+  float m, l, c;
+  uint32_t koff[KS], voff[DT][2];
+
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (BF)
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  __device__ __forceinline__ void init(const uint16_t* qp, int D, float scale, int lane) {
+    const int n = lane & 15, g = lane >> 4, a = (lane >> 2) & 3, b = lane & 3;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int d = ks * 32 + 8 * g;
+      const u32x4 z = {0, 0, 0, 0};
+      q[ks] = d < D ? *reinterpret_cast<const u32x4*>(qp + d) : z;
+      koff[ks] = n * ROWB + (((4 * ks + g) ^ swz<DP>(n)) << 4);
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 4 * g + a + 16 * i;
+        voff[dt][i] = k * ROWB + (((2 * dt + (b >> 1)) ^ swz<DP>(k)) << 4) + (b & 1) * 8;
+      }
+    }
+    m = kNone;
+    l = 0.f;
+    c = scale * kLog2e;
+  }
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) __asm__ __volatile__("" : "+v"(q[s]));
+  }
+  __device__ __forceinline__ void keys(const lds_u8* kt, Keys& k) {
+    typedef const __attribute__((address_space(3))) u32x4 lds_u32x4;
+    u32x4 kf[2 * KS];
+#pragma unroll
+    for (int n = 0; n < 2 * KS; ++n) kf[n] = *reinterpret_cast<lds_u32x4*>(kt + (n & 1) * 16 * ROWB + koff[n >> 1]);
+    k.s[0] = k.s[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 2 * KS; ++n) k.s[n & 1] = mma(kf[n], q[n >> 1], k.s[n & 1]);
+  }
+  static __device__ __forceinline__ void hide(Keys& k, uint32_t seen, int lane) {
+    seen >>= 4 * (lane >> 4);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) k.s[t][r] = (seen >> (16 * t + r)) & 1 ? k.s[t][r] : -INFINITY;
+  }
+  __device__ __forceinline__ void exps(Keys& k, P& p) {
+    float mx = k.s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, k.s[t][r]);
+    if (__any(mx * c > m + kSlack)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m, mx * c), f = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[dt] *= f;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        k.s[t][r] = __builtin_amdgcn_exp2f(fmaf(k.s[t][r], c, -m));
+        l += k.s[t][r];
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t hi, lo;
+        split_pair<BF>(k.s[t][2 * r], k.s[t][2 * r + 1], hi, lo);
+        p.hi[2 * t + r] = hi;
+        p.lo[2 * t + r] = lo;
+      }
+    }
+  }
+  __device__ __forceinline__ void product(const lds_u8* vt, const P& p) {
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const uint2 w0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + voff[dt][0])));
+      const uint2 w1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vt + voff[dt][1])));
+      const u32x4 vf = {w0.x, w0.y, w1.x, w1.y};
+      o[dt] = mma(vf, p.hi, o[dt]);
+      o[dt] = mma(vf, p.lo, o[dt]);
+    }
+  }
+  static __device__ __forceinline__ float prob(const Keys& k, int kk, int lane) {
+    float pk = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pk = i == ((kk >> 4) << 2 | (kk & 3)) ? k.s[i >> 2][i & 3] : pk;
+    return __shfl(pk, (kk >> 2 & 3) * 16 + (lane & 15));
+  }
+  __device__ __forceinline__ void add_value(const lds_u8* vt, int kk, float pk, int lane) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[dt][r] = fmaf(pk, value_at<BF, DP>(vt, kk, 16 * dt + 4 * (lane >> 4) + r), o[dt][r]);
+  }
+  __device__ __forceinline__ float total() const {
+    const float s = l + __shfl_xor(l, 16);
+    return s + __shfl_xor(s, 32);
+  }
+  template <class F>
+  __device__ __forceinline__ void each_quad(int lane, F&& f) const {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) f(4 * dt + (lane >> 4), make_float4(o[dt][0], o[dt][1], o[dt][2], o[dt][3]));
+  }
+};
+
 // Copies of this wave's NI instructions of a tile, 64 / CPR rows each, from
 // row `row0` of the tile on; K and V lie alike, so one set of offsets serves
 // both.
@@ -409,18 +607,10 @@ struct TileCopy {
     const int in_page = (1 << src.shift) - 1;
     if (each) {
       const uint64_t from = starts(src, base, pages, first, key0, end, row0, lane);
-      if (key0 + row0 + NI * RPI <= end) {
+      uint32_t o[NI];
+      offsets(src, key0, end, row0, lane, o);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) one(from, off[i % NV], i, lds + row0 * DP * 2);
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-          const int row = row0 + i * RPI, have = max(end - 1 - (key0 + row), 0);
-          const uint32_t o = static_cast<uint32_t>(min(lane / CPR, have)) * static_cast<uint32_t>(src.row) +
-                             chunk(row + lane / CPR, lane, D) * 16;
-          copy_to_lds(start(from, i), o, lds + row * DP * 2);
-        }
-      }
+      for (int i = 0; i < NI; ++i) one(from, o[i], i, lds + row0 * DP * 2);
       return;
     }
 #pragma unroll 1
@@ -446,13 +636,9 @@ __device__ __forceinline__ bool load_pages(const KeySource& src, int k0, int k1,
   return __syncthreads_or(bad);
 }
 
-// Key j of subtile register i.
-__device__ __forceinline__ int key_of(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
-
-template <bool BF, int DP>
+template <bool BF, int DP, class Tile>
 struct Attn {
   typedef RowTile<BF, DP, false> WideTile;
-  typedef RowTile<BF, DP, true> NarrowTile;
   static constexpr int CPR = DP / 8, RPI = 64 / CPR, ROWB = DP * 2;
   static constexpr int kWideKeys = DP == 256 ? 32 : 64;        // keys of a wide tile
   static constexpr int kTileBytes = kWideKeys * ROWB;          // its K or V
@@ -607,7 +793,7 @@ struct Attn {
     }
   }
 
-  // 32 rows against keys [k0, k1) of the prefix or of a sequence's suffix:
+  // A row tile against keys [k0, k1) of the prefix or of a sequence's suffix:
   // each wave takes every fourth tile of 32 keys through its own LDS, with no
   // barrier; a tile's K and V are copied again as soon as the wave has read
   // them.  The waves' parts are joined at the end.
@@ -618,7 +804,7 @@ struct Attn {
     const qmv_attn_args& a = g.a;
     const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = a.head_dim;
     const int G = g.p.groups, M = nrows * G;
-    const int mi = min(r0 + (lane & 31), M - 1), ri = quotient(mi, g.groups);
+    const int mi = min(r0 + lane % Tile::kRows, M - 1), ri = quotient(mi, g.groups);
     const int row = rbase + ri, head = hk * G + remainder_of(mi, ri, g.groups);
     bool bad = false;
     if (src.table) bad = load_pages(src, k0, k1, pages);
@@ -636,7 +822,7 @@ struct Attn {
       cp.copy(src, src.k, pg, first, each, k0 + wave * 32, k1, 0, klds, lane, D);
       cp.copy(src, src.v, pg, first, each, k0 + wave * 32, k1, 0, vlds, lane, D);
     }
-    NarrowTile t;
+    Tile t;
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     uint64_t mask = a.tree_mask && draft0 < k1 ? a.tree_mask[row] : 0;
     t.arrived();
@@ -645,9 +831,9 @@ struct Attn {
     for (int tile = wave; tile < tiles; tile += 4) {
       const int key0 = k0 + tile * 32;
       const bool more = tile + 4 < tiles;
-      f32x16 s[1];
+      typename Tile::Keys s;
       wait_copies<NI>();  // outstanding: this tile's K, its V
-      t.template scores<1>(kt, s);
+      t.keys(kt, s);
       wait_lds();
       if (more) cp.copy(src, src.k, pg, first, each, key0 + 128, k1, 0, klds, lane, D);
       const bool partly = key0 + 32 > min(draft0, k1) || bad;  // some rows do not see some of the keys
@@ -664,18 +850,13 @@ struct Attn {
           const int key = min(key0 + (lane & 31), k1 - 1);
           seen &= ~static_cast<uint32_t>(__ballot(pages[(key >> src.shift) - first] < 0));
         }
-        seen >>= 4 * (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[0][i] = (seen >> (8 * (i >> 2) + (i & 3))) & 1 ? s[0][i] : -INFINITY;
+        t.hide(s, seen, lane);
       }
-      float mx;
-      if (t.template moves<1>(s, mx)) t.move(mx);
-      typename NarrowTile::template Probs<1> p;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) t.template exp_pair<1>(s, n, p);
+      typename Tile::P p;
+      t.exps(s, p);
       if (more) wait_copies<NI>(); else wait_copies<0>();
-      if (partly) unseen_values(t, s[0], vt, lane, bad ? 0 : min(draft0, k1) - key0, D);
-      t.template values<1>(vt, p);
+      if (partly) unseen_values(t, s, vt, lane, bad ? 0 : min(draft0, k1) - key0);
+      t.product(vt, p);
       wait_lds();
       if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane, D);
     }
@@ -684,28 +865,22 @@ struct Attn {
     // The waves' parts: [wave][row][DP] in the tiles' place, maxima and sums in `pages`.
     float* parts = reinterpret_cast<float*>(smem);
     float2* ml = reinterpret_cast<float2*>(pages);
-    const float l = t.l + __shfl_xor(t.l, 32);
-    {
-      // rows are 16-byte chunks, permuted by the row against bank conflicts
-      float4* p = reinterpret_cast<float4*>(parts + (wave * 32 + (lane & 31)) * DP);
-#pragma unroll
-      for (int dt = 0; dt < NarrowTile::DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[(8 * dt + 2 * i + (lane >> 5)) ^ (lane & 7)] =
-              make_float4(t.o[dt][4 * i], t.o[dt][4 * i + 1], t.o[dt][4 * i + 2], t.o[dt][4 * i + 3]);
-      if (lane < 32) ml[wave * 32 + lane] = make_float2(t.m, l);
-    }
+    const float l = t.total();
+    // (rows are 16-byte chunks, permuted by the row against bank conflicts)
+    constexpr int kRows = Tile::kRows;
+    float4* mine = reinterpret_cast<float4*>(parts + (wave * kRows + lane % kRows) * DP);
+    t.each_quad(lane, [&](int ch, float4 v) { mine[ch ^ (lane & 7)] = v; });
+    if (lane < kRows) ml[wave * kRows + lane] = make_float2(t.m, l);
     __syncthreads();
     constexpr int kQuads = DP / 4;
-    for (int e = threadIdx.x; e < min(32, M - r0) * kQuads; e += 256) {
+    for (int e = threadIdx.x; e < min(kRows, M - r0) * kQuads; e += 256) {
       const int r = e / kQuads, ch = e % kQuads, m = r0 + r;
       if (ch * 4 >= D) continue;
       float2 w[4];
       float mx = kNone;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        w[k] = ml[k * 32 + r];
+        w[k] = ml[k * kRows + r];
         mx = fmaxf(mx, w[k].x);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -713,7 +888,7 @@ struct Attn {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float f = __builtin_amdgcn_exp2f(w[k].x - mx);
-        const float4 v = reinterpret_cast<const float4*>(parts + (k * 32 + r) * DP)[ch ^ (r & 7)];
+        const float4 v = reinterpret_cast<const float4*>(parts + (k * kRows + r) * DP)[ch ^ (r & 7)];
         sum.x = fmaf(f, v.x, sum.x);
         sum.y = fmaf(f, v.y, sum.y);
         sum.z = fmaf(f, v.z, sum.z);
@@ -732,8 +907,8 @@ struct Attn {
   // end or on pages outside the pool by none), and 0 x infinity or NaN is not
   // 0: values of tile rows from `from` on that are not finite are added here
   // to the rows that see them, and zeroed for the product.
-  static __device__ __forceinline__ void unseen_values(NarrowTile& t, const f32x16& p, lds_u8* vt, int lane, int from,
-                                                       int D) {
+  static __device__ __forceinline__ void unseen_values(Tile& t, const typename Tile::Keys& s, lds_u8* vt, int lane,
+                                                       int from) {
     const int r = lane & 31;
     constexpr uint16_t kExp = BF ? 0x7F80u : 0x7C00u;  // (columns past D, where D is not DP, are some of the row's)
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -753,23 +928,8 @@ struct Attn {
     while (rows) {
       const int kk = __builtin_ctz(rows);
       rows &= rows - 1;
-      const int ri = ((kk >> 3) << 2) | (kk & 3);
-      float pk = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk = i == ri ? p[i] : pk;
-      const float other = __shfl_xor(pk, 32);
-      pk = (lane >> 5) == ((kk >> 2) & 1) ? pk : other;
-      const bool seen = !(pk == 0.f);
-#pragma unroll
-      for (int dt = 0; dt < NarrowTile::DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int d = 32 * dt + key_of(i, lane);
-          const uint32_t b = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
-              vt + kk * ROWB + (((d >> 3) ^ swz<DP>(kk)) << 4) + (d & 7) * 2);
-          const float v = BF ? bf16_to_f32(b) : f16_to_f32(b);
-          t.o[dt][i] = seen ? fmaf(pk, v, t.o[dt][i]) : t.o[dt][i];
-        }
+      const float pk = t.prob(s, kk, lane);
+      if (!(pk == 0.f)) t.add_value(vt, kk, pk, lane);
       order_memory();
       if (lane < CPR) zero_chunk(vt + kk * ROWB + lane * 16);
       order_memory();
@@ -777,9 +937,9 @@ struct Attn {
   }
 };
 
-template <bool BF, int DP>
+template <bool BF, int DP, class Tile>
 __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(const AttnKernelArgs g) {
-  typedef Attn<BF, DP> A;
+  typedef Attn<BF, DP, Tile> A;
   extern __shared__ __attribute__((aligned(16))) uint8_t attn_lds[];
   int* pages = reinterpret_cast<int*>(attn_lds + A::kLds);
   const qmv_attn_args& a = g.a;
@@ -818,7 +978,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(cons
     const int len = min(max(a.suffix_len[b], 0), static_cast<int>(a.max_suffix));
     if (rbase < 0 || end > n || rbase >= end) return;
     n = min(end - rbase, a.max_rows);
-    if (rt * 32 >= n * g.p.groups) return;
+    if (rt * Tile::kRows >= n * g.p.groups) return;
     k0 = split * g.p.sseg;
     k1 = min(k0 + g.p.sseg, len);
     if (k0 >= k1) return;
@@ -833,7 +993,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(cons
   if (g.p.wide && prefix)
     A::wide(g, src, slot, hk, rt, k0, k1, attn_lds, pages);
   else
-    A::narrow(g, src, slot, hk, rbase, n, rt * 32, k0, k1, draft0, attn_lds, pages);
+    A::narrow(g, src, slot, hk, rbase, n, rt * Tile::kRows, k0, k1, draft0, attn_lds, pages);
 }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -996,11 +1156,13 @@ static AttnPlan plan_attn(const qmv_attn_args& a) {
   const bool pages_fit = a.page_size >= rpi && a.page_row < near;
   p.each = pages_fit;
   p.wide = M > 64 && (a.prefix_pages ? pages_fit : a.prefix_row < near);
-  p.row_tiles = ceil_div(M, p.wide ? 128 : 32);
+  const int64_t suffix_rows = std::min<int64_t>(a.max_rows, a.rows) * p.groups;
+  p.rows = suffix_rows <= 16 && (p.wide || M <= 16 || a.prefix_len == 0) ? 16 : 32;
+  p.row_tiles = ceil_div(M, p.wide ? 128 : p.rows);
   const double width = (a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256) / 128.0;
   double suffix_us = 0.0;
   if (a.max_suffix > 0) {
-    p.srow_tiles = ceil_div(std::min<int64_t>(a.max_rows, a.rows) * p.groups, 32);
+    p.srow_tiles = ceil_div(suffix_rows, p.rows);
     // (sequences are seldom all as long as the longest: half the ranges are taken to be empty)
     const int64_t units = static_cast<int64_t>(a.nseq) * a.kv_heads * p.srow_tiles;
     const int64_t n = std::max<int64_t>(
@@ -1037,20 +1199,24 @@ size_t attn_workspace(const qmv_attn_args& a) {
   return ml_bytes(a, p) + static_cast<size_t>(p.psplits + p.ssplits) * a.rows * a.heads * a.head_dim * sizeof(float);
 }
 
-template <bool BF, int DP>
+template <bool BF, int DP, class Tile>
 static hipError_t launch_parts(const AttnKernelArgs& g, hipStream_t s) {
-  constexpr int lds = Attn<BF, DP>::kLds + kMaxPages * 4;
+  constexpr int lds = Attn<BF, DP, Tile>::kLds + kMaxPages * 4;
   const unsigned grid = static_cast<unsigned>(g.p.prefix_wgs + g.p.suffix_wgs);
-  if (grid) hipLaunchKernelGGL((attn_parts_kernel<BF, DP>), dim3(grid), dim3(256), lds, s, g);
+  if (grid) hipLaunchKernelGGL((attn_parts_kernel<BF, DP, Tile>), dim3(grid), dim3(256), lds, s, g);
   return hipGetLastError();
 }
 
 template <bool BF>
 static hipError_t attn_typed(const AttnKernelArgs& g, hipStream_t s) {
   const int D = g.a.head_dim;
-  const hipError_t e = D <= 64    ? launch_parts<BF, 64>(g, s)
-                       : D <= 128 ? launch_parts<BF, 128>(g, s)
-                                  : launch_parts<BF, 256>(g, s);
+  const auto parts = [&](auto width) {
+    constexpr int DP = decltype(width)::value;
+    return g.p.rows == 16 ? launch_parts<BF, DP, Narrow16<BF, DP>>(g, s) : launch_parts<BF, DP, Narrow32<BF, DP>>(g, s);
+  };
+  const hipError_t e = D <= 64    ? parts(std::integral_constant<int, 64>{})
+                       : D <= 128 ? parts(std::integral_constant<int, 128>{})
+                                  : parts(std::integral_constant<int, 256>{});
   if (e != hipSuccess) return e;
   // Few rows of many parts: four waves to a row.
   const int64_t all = g.a.rows * g.a.heads;

@@ -128,6 +128,25 @@ def test_head_shapes(heads, kv, dim, dtype):
     s.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,suffix", [([1], [40]), ([2], [2]), ([1, 1], [100, 33])])
+@pytest.mark.parametrize("heads,kv,dim", HEADS)
+def test_few_rows(heads, kv, dim, rows, suffix, dtype):
+    # at most 16 rows of a key head
+    say(f"attn heads {heads}/{kv} dim {dim} rows {rows} {dtype}")
+    s = Step(dtype, heads, kv, dim, 171, rows, suffix, page=8, tree=rows == [2], seed=dim + 1)
+    s.run()
+    s.check()
+
+
+def test_few_rows_beside_many():
+    # the prefix's rows are many, each sequence's few
+    for seqs in (9, 40):
+        s = Step("f16", 14, 2, 128, 300, [1] * seqs, [1 + 13 * i % 70 for i in range(seqs)], page=8, seed=seqs)
+        s.run()
+        s.check()
+
+
 @pytest.mark.parametrize("prefix", [0, 1, 31, 32, 33, 63, 64, 65, 127, 257, 1030])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_prefix_lengths(prefix, dtype):
@@ -180,8 +199,8 @@ def test_prefix_in_pages():
 
 
 def test_pages_outside_the_pool_are_not_seen():
-    for rows in ([1, 2, 1], [8, 5, 8]):
-        s = Step("bf16", 8, 2, 64, 33, rows, [50, 37, 48], page=16, seed=8,
+    for rows, heads in (([1, 2, 1], 8), ([8, 5, 8], 8), ([1, 1, 1], 4)):
+        s = Step("bf16", heads, 2, 64, 33, rows, [50, 37, 48], page=16, seed=8,
                  bad=[(0, 1, -1), (1, 0, 1 << 30), (2, 0, -(1 << 31)), (2, 1, 9999), (2, 2, 77)])
         s.run()
         s.check()
@@ -216,8 +235,8 @@ def test_suffix_shorter_than_the_rows():
 
 def test_unseen_drafts_may_hold_anything():
     # tree: rows see only themselves; the other drafts' keys and values are NaN and infinity for them
-    for rows, dim in [([4, 3], 64), ([5, 4], 128)]:
-        s = Step("bf16", 6, 2, dim, 30, rows, [12, 9], page=8, tree=True, seed=13, poison=True)
+    for rows, dim, heads in [([4, 3], 64, 6), ([5, 4], 128, 6), ([3, 2], 64, 6), ([4, 3], 72, 4)]:
+        s = Step("bf16", heads, 2, dim, 30, rows, [12, 9], page=8, tree=True, seed=13, poison=True)
         s.mask[:] = 1  # everyone sees the first row's token alone
         for b, (n, length) in enumerate(zip(rows, [12, 9])):
             for i, x in zip(range(1, n), [float("nan"), float("inf"), float("-inf"), float("nan")]):
@@ -229,7 +248,12 @@ def test_unseen_drafts_may_hold_anything():
 
 
 def test_a_later_draft_of_nan_stays_with_the_rows_that_see_it():
-    s = Step("f16", 4, 2, 64, 30, [4, 2], [12, 6], page=8, seed=14)
+    for heads in (4, 6):
+        later_draft_of_nan(heads)
+
+
+def later_draft_of_nan(heads):
+    s = Step("f16", heads, 2, 64, 30, [4, 2], [12, 6], page=8, seed=14)
     j = 12 - 1  # the last row's own key and value
     clean = s.run().clone()
     s.v_pages[s.table[0, j // 8], j % 8] = float("inf")
