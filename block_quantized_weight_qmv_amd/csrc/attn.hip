@@ -97,7 +97,7 @@ struct AttnPlan {
 struct AttnKernelArgs {
   qmv_attn_args a;
   AttnPlan p;
-  FastDiv groups, pairs, kv_heads, srow_tiles, ssplits, heads;
+  FastDiv groups, pairs, kv_heads, srow_tiles, nseq, heads;
   float* po;         // [slot][row * heads + head][D]
   float2* pml;       // [slot][row * heads + head]: maximum (log2), sum
 };
@@ -964,15 +964,17 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(cons
     k1 = draft0 = min(k0 + g.p.pseg, static_cast<int>(a.prefix_len));
     src.table = a.prefix_pages;
   } else {
-    // a sequence's key heads share lines: 8 x kv_heads workgroups go to the 8
-    // XCDs as 8 sequences' heads
-    const int eights = quotient(id >> 3, g.kv_heads), first = eights * 8 * a.kv_heads;
-    if (first + 8 * a.kv_heads <= static_cast<int>(g.p.suffix_wgs))
-      id = first + (id & 7) * a.kv_heads + remainder_of(id >> 3, eights, g.kv_heads);
-    const int q1 = quotient(id, g.kv_heads), q2 = quotient(q1, g.srow_tiles), b = quotient(q2, g.ssplits);
+    // A sequence's key heads share lines: of 8 x kv_heads workgroups, those of
+    // one XCD are one sequence's heads (another place of the eight each time,
+    // so that no XCD gets all the long sequences of a regular batch).  First
+    // ranges come before second ones, which only long sequences have.
+    const int eights = quotient(id >> 3, g.kv_heads), base = eights * 8 * a.kv_heads;
+    if (base + 8 * a.kv_heads <= static_cast<int>(g.p.suffix_wgs))
+      id = base + ((id + eights) & 7) * a.kv_heads + remainder_of(id >> 3, eights, g.kv_heads);
+    const int q1 = quotient(id, g.kv_heads), q2 = quotient(q1, g.srow_tiles), split = quotient(q2, g.nseq);
     hk = remainder_of(id, q1, g.kv_heads);
     rt = remainder_of(q1, q2, g.srow_tiles);
-    const int split = remainder_of(q2, b, g.ssplits);
+    const int b = remainder_of(q2, split, g.nseq);
     const int end = a.row_start[b + 1];
     rbase = a.row_start[b];
     const int len = min(max(a.suffix_len[b], 0), static_cast<int>(a.max_suffix));
@@ -1244,7 +1246,7 @@ hipError_t attn(const qmv_attn_args& a, void* ws, hipStream_t s) {
   g.pairs = fast_div(std::max<int64_t>(1, static_cast<int64_t>(a.kv_heads) * g.p.psplits));
   g.kv_heads = fast_div(a.kv_heads);
   g.srow_tiles = fast_div(std::max(1, g.p.srow_tiles));
-  g.ssplits = fast_div(std::max(1, g.p.ssplits));
+  g.nseq = fast_div(a.nseq);
   g.heads = fast_div(a.heads);
   g.pml = static_cast<float2*>(ws);
   g.po = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ml_bytes(a, g.p));
