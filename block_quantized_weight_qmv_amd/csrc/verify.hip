@@ -24,10 +24,12 @@ namespace qmv {
 
 // The first launch: a wave's piece of a row, and its workgroup's four.
 constexpr int kRowThreads = 256, kRowPer = 32, kPiece = 64 * kRowPer;
-// The second: a slice, of which a workgroup takes one or, where there are
-// sequences enough to fill the chip, several.
-constexpr int kThreads = 1024, kWaves = kThreads / 64, kPer = 8, kSlice = kThreads * kPer;
-static_assert(kSlice % kPiece == 0, "a slice is whole pieces");
+// The second: a workgroup's slice, a piece again (one or, where there are
+// sequences enough to fill the chip, several of them).  Four 64-bit weights to
+// a thread: they are the longest step of a lone sequence (with 8192 tokens to
+// 1024 threads of one compute unit, 12.3 us against DRAWONE).
+constexpr int kThreads = 512, kWaves = kThreads / 64, kPer = 4;
+static_assert(kThreads * kPer == kPiece, "a slice is a piece");
 
 struct PieceStat {
   double sum;   // of e^((l - max) / T); of the infinities' ones where max is +inf
@@ -37,10 +39,10 @@ struct PieceStat {
 
 struct VerifyArgs {
   qmv_verify_args a;
-  int pieces, slices;
-  int span;          // slices of a workgroup of the second launch
+  int pieces;        // of a row
+  int span;          // pieces of a workgroup of the second launch
   PieceStat* stat;   // [row][piece]
-  double* part;      // [sequence][slice]: the drawing row's weights
+  double* part;      // [sequence][piece]: the drawing row's weights
   uint32_t* done;    // [sequence]: workgroups that have left their part
 };
 
@@ -107,17 +109,32 @@ __device__ __forceinline__ float logit(const qmv_verify_args& a, int64_t row, in
   return no_nan(Logits<DT>::get(&v, 0));
 }
 
+// Values of one load: 16 bytes, or a thread's N values where they are fewer.
+template <int DT, int N>
+constexpr int values_of_load() {
+  constexpr int k = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+  return N < k ? N : k;
+}
+
 // N consecutive values from place i0 of a row of n, at any alignment of its
 // type; places from n on give `past`.
 template <int DT, int N>
 __device__ __forceinline__ void load_row(const void* row, int64_t i0, int64_t n, float past, float* v) {
   typedef typename Logits<DT>::word word;
-  constexpr int kV = 16 / sizeof(word);
+  constexpr int kV = values_of_load<DT, N>();
+  static_assert(N % kV == 0 && (kV * sizeof(word) == 16 || kV * sizeof(word) == 8), "loads of 8 or 16 bytes");
 #pragma unroll
   for (int k = 0; k < N; k += kV) {
     if (i0 + k + kV <= n) {
-      const uint4 w = ld16_any(reinterpret_cast<const uint8_t*>(static_cast<const word*>(row) + i0 + k));
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(static_cast<const word*>(row) + i0 + k);
+      uint32_t x[4];
+      if constexpr (kV * sizeof(word) == 16) {
+        const uint4 w = ld16_any(at);
+        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+      } else {
+        const uint2 w = ld8_any(at);
+        x[0] = w.x, x[1] = w.y;
+      }
 #pragma unroll
       for (int j = 0; j < kV; ++j) v[k + j] = Logits<DT>::get(x, j);
     } else {
@@ -133,17 +150,17 @@ __device__ __forceinline__ void load_row(const void* row, int64_t i0, int64_t n,
   }
 }
 
-// The place of value j of thread t of THREADS, 16 bytes a thread at a time.
-template <int DT, int THREADS>
+// The place of value j of the N of thread t of THREADS, one load a thread at a time.
+template <int DT, int THREADS, int N>
 __device__ __forceinline__ int place(int t, int j) {
-  constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+  constexpr int kV = values_of_load<DT, N>();
   return (j / kV) * THREADS * kV + t * kV + j % kV;
 }
 template <int DT, int THREADS, int N>
 __device__ __forceinline__ void load_pieces(const void* row, int64_t s0, int t, int64_t n, float past, float* v) {
-  constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+  constexpr int kV = values_of_load<DT, N>();
 #pragma unroll
-  for (int k = 0; k < N; k += kV) load_row<DT, kV>(row, s0 + place<DT, THREADS>(t, k), n, past, v + k);
+  for (int k = 0; k < N; k += kV) load_row<DT, kV>(row, s0 + place<DT, THREADS, N>(t, k), n, past, v + k);
 }
 
 // v of the lane that a DPP control names (lanes without one, or outside the
@@ -239,7 +256,7 @@ __global__ void __launch_bounds__(kRowThreads) verify_rows_kernel(const VerifyAr
   if (t == 0.f) {  // only the first place of the maximum counts
     best = INT32_MAX;
 #pragma unroll
-    for (int j = kRowPer - 1; j >= 0; --j) best = v[j] == m ? place<DT, 64>(lane, j) : best;
+    for (int j = kRowPer - 1; j >= 0; --j) best = v[j] == m ? place<DT, 64, kRowPer>(lane, j) : best;
     best = wave_fold(best, [](int x, int y) { return min(x, y); });
   } else if (m == INFINITY) {
 #pragma unroll
@@ -264,8 +281,8 @@ struct RowStat {
 __device__ __forceinline__ RowStat row_stat(const VerifyArgs& g, int row, double c_t) {
   const PieceStat* st = g.stat + static_cast<int64_t>(row) * g.pieces;
   const int lane = __lane_id();
-  // (the first pieces are kept, 192 of them)
-  constexpr int kKeep = 3;
+  // (the first pieces are kept, 128 of them)
+  constexpr int kKeep = 2;
   PieceStat x[kKeep];
   float m = -INFINITY;
 #pragma unroll
@@ -344,18 +361,14 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     bool plain = false;
     double total = 0.0;
     auto part = [&](int s) {
-      if (s >= g.slices) return 0.0;
-      if (!plain) return __hip_atomic_load(g.part + static_cast<int64_t>(b) * g.slices + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      double w = 0.0;
-      for (int k = s * (kSlice / kPiece); k < min((s + 1) * (kSlice / kPiece), g.pieces); ++k) {
-        const PieceStat st = g.stat[d.row * g.pieces + k];
-        w += st.sum * weight(st.max, d.max, d.c_t);
-      }
-      return w;
+      if (s >= g.pieces) return 0.0;
+      if (!plain) return __hip_atomic_load(g.part + static_cast<int64_t>(b) * g.pieces + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const PieceStat st = g.stat[d.row * g.pieces + s];
+      return st.sum * weight(st.max, d.max, d.c_t);
     };
     for (;;) {
       total = 0.0;
-      for (int s0 = 0; s0 < g.slices; s0 += 64) total += wave_fold(part(s0 + lane), add);
+      for (int s0 = 0; s0 < g.pieces; s0 += 64) total += wave_fold(part(s0 + lane), add);
       if (total > 0.0 || plain) break;
       plain = true;  // nothing is left over q: the target's own probabilities
     }
@@ -363,7 +376,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     double before = 0.0;
     int slice = -1, last = 0;
     double base = 0.0;
-    for (int s0 = 0; s0 < g.slices && slice < 0; s0 += 64) {
+    for (int s0 = 0; s0 < g.pieces && slice < 0; s0 += 64) {
       const double v = part(s0 + lane), c = wave_scan(v) + before;
       const uint64_t some = __ballot(v > 0.0), over = __ballot(c > goal && v > 0.0);
       if (some) last = s0 + 63 - __builtin_clzll(some);
@@ -386,7 +399,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     d.hot = -1;
   }
   // contiguous places to a thread
-  const int64_t i0 = static_cast<int64_t>(sh_slice) * kSlice + tid * kPer;
+  const int64_t i0 = static_cast<int64_t>(sh_slice) * kPiece + tid * kPer;
   const void* row = static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row;
   float v[kPer], q[kPer];
   load_row<DT, kPer>(row, i0, a.vocab, -INFINITY, v);
@@ -485,26 +498,26 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     // (no barrier between slices: the next one's loads run under this one's sums)
     constexpr int kGroup = 4;
     __shared__ double sums[kGroup][kWaves];
-    const int last_slice = min(first_slice + g.span, g.slices);
+    const int last_slice = min(first_slice + g.span, g.pieces);
     for (int s0 = first_slice; s0 < last_slice; s0 += kGroup) {
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) {
         if (s0 + k >= last_slice) break;
-        const int64_t i0 = static_cast<int64_t>(s0 + k) * kSlice;
+        const int64_t i0 = static_cast<int64_t>(s0 + k) * kPiece;
         float v[kPer], q[kPer];
         load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, i0,
                                         tid, a.vocab, -INFINITY, v);
         if (d.q) {
           // (in the places that v holds)
-          constexpr int kV = 16 / static_cast<int>(sizeof(typename Logits<DT>::word));
+          constexpr int kV = values_of_load<DT, kPer>();
 #pragma unroll
           for (int j = 0; j < kPer; j += kV)
-            load_row<QMV_F32, kV>(d.q, i0 + place<DT, kThreads>(tid, j), a.vocab, 0.f, q + j);
+            load_row<QMV_F32, kV>(d.q, i0 + place<DT, kThreads, kPer>(tid, j), a.vocab, 0.f, q + j);
         }
         double w[kPer], s = 0.0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = no_nan(v[j]);
-        draw_weights(d, v, q, a.vocab, w, [&](int j) { return i0 + place<DT, kThreads>(tid, j); });
+        draw_weights(d, v, q, a.vocab, w, [&](int j) { return i0 + place<DT, kThreads, kPer>(tid, j); });
 #pragma unroll
         for (int j = 0; j < kPer; ++j) s += w[j];
         s = wave_fold(s, add);
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
         double s = 0.0;
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) s += sums[tid][k];
-        __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.slices + s0 + tid, s, __ATOMIC_RELAXED,
+        __hip_atomic_store(g.part + static_cast<int64_t>(b) * g.pieces + s0 + tid, s, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
       }
       __syncthreads();
@@ -542,12 +555,11 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
 }
 
 static int pieces_of(const qmv_verify_args& a) { return static_cast<int>((a.vocab + kPiece - 1) / kPiece); }
-static int slices_of(const qmv_verify_args& a) { return static_cast<int>((a.vocab + kSlice - 1) / kSlice); }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t verify_workspace(const qmv_verify_args& a) {
   return up256(a.rows * static_cast<size_t>(pieces_of(a)) * sizeof(PieceStat)) +
-         up256(a.nseq * static_cast<size_t>(slices_of(a)) * sizeof(double)) + up256(a.nseq * 4);
+         up256(a.nseq * static_cast<size_t>(pieces_of(a)) * sizeof(double)) + up256(a.nseq * 4);
 }
 
 template <int DT>
@@ -557,7 +569,7 @@ static hipError_t verify_typed(const VerifyArgs& g, hipStream_t s) {
                      dim3(kRowThreads), 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(verify_draw_kernel<DT>, dim3((g.slices + g.span - 1) / g.span, g.a.nseq), dim3(kThreads), 0, s, g);
+  hipLaunchKernelGGL(verify_draw_kernel<DT>, dim3((g.pieces + g.span - 1) / g.span, g.a.nseq), dim3(kThreads), 0, s, g);
   return hipGetLastError();
 }
 
@@ -565,14 +577,13 @@ hipError_t verify(const qmv_verify_args& a, void* ws, hipStream_t s) {
   VerifyArgs g;
   g.a = a;
   g.pieces = pieces_of(a);
-  g.slices = slices_of(a);
-  // about one workgroup a compute unit
-  g.span = static_cast<int>(std::min<int64_t>(g.slices, (static_cast<int64_t>(g.slices) * a.nseq + 255) / 256));
+  // about two workgroups a compute unit
+  g.span = static_cast<int>(std::min<int64_t>(g.pieces, (static_cast<int64_t>(g.pieces) * a.nseq + 511) / 512));
   uint8_t* p = static_cast<uint8_t*>(ws);
   g.stat = reinterpret_cast<PieceStat*>(p);
   p += up256(static_cast<size_t>(a.rows) * g.pieces * sizeof(PieceStat));
   g.part = reinterpret_cast<double*>(p);
-  p += up256(static_cast<size_t>(a.nseq) * g.slices * sizeof(double));
+  p += up256(static_cast<size_t>(a.nseq) * g.pieces * sizeof(double));
   g.done = reinterpret_cast<uint32_t*>(p);
   switch (a.logits_dtype) {
     case QMV_F32: return verify_typed<QMV_F32>(g, s);
