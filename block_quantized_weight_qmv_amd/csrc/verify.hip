@@ -4,17 +4,18 @@
 //
 // Two launches.  The first cuts every row of logits into pieces of kPiece and
 // leaves each piece's maximum, its first place and the sum of
-// e^((l - maximum) / T).  In the second, one workgroup per sequence and slice:
-// every one of them settles, from those sums, which drafts are accepted, adds
-// up its slice of the row that draws, and the last of a sequence to finish
-// finds the token in the slice that holds it.
+// e^((l - maximum) / T).  In the second, every workgroup of a sequence settles
+// from those sums which drafts are accepted and adds up its pieces of the row
+// that draws; the last of a sequence to finish finds the token in the piece
+// that holds it.  (A row of accepted drafts draws from p, whose pieces are
+// added up already: one workgroup does it.)
 //
 // Exponentials and sums are in 64 bits.  A draw compares a running sum of up
 // to 2^24 probabilities with u times their total; in 32 bits their errors
 // would move about one draw in a hundred over 152064 flat probabilities to a
-// neighbouring token.  The 64-bit exponentials, about twenty instructions
-// each, run beside the reads of the logits, which bound the first launch:
-// PERF_ROWS
+// neighbouring token.  At eighteen 64-bit instructions of 8 clocks each, the
+// exponentials bound the first launch: 288 rows of 152064 fp32 logits take 47
+// us (their reads alone, 175 MB, 28 us at 6.3 TB/s).
 #include <algorithm>
 
 #include "device_util.h"
@@ -27,7 +28,7 @@ constexpr int kRowThreads = 256, kRowPer = 32, kPiece = 64 * kRowPer;
 // The second: a workgroup's slice, a piece again (one or, where there are
 // sequences enough to fill the chip, several of them).  Four 64-bit weights to
 // a thread: they are the longest step of a lone sequence (with 8192 tokens to
-// 1024 threads of one compute unit, 12.3 us against DRAWONE).
+// 1024 threads of one compute unit, 12.3 us against 8.6).
 constexpr int kThreads = 512, kWaves = kThreads / 64, kPer = 4;
 static_assert(kThreads * kPer == kPiece, "a slice is a piece");
 
@@ -348,17 +349,18 @@ __device__ __forceinline__ double wave_scan(double v) {
 }
 
 // The token: the first whose running sum passes u times the total (by the
-// whole workgroup).  plain: p itself, from the pieces' sums.
+// whole workgroup).  target: from the target's own probabilities, whose pieces
+// the first launch added up.
 template <int DT>
-__device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw& d0, float u) {
+__device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw& d0, float u, bool target) {
   const qmv_verify_args& a = g.a;
   const int tid = threadIdx.x, lane = __lane_id(), wave = tid >> 6;
   __shared__ double sh_goal;
-  __shared__ int sh_slice, sh_plain, sh_first[kWaves], sh_last[kWaves];
+  __shared__ int sh_piece, sh_plain, sh_first[kWaves], sh_last[kWaves];
   __shared__ double sh_sum[kWaves];
   Draw d = d0;
   if (wave == 0) {
-    bool plain = false;
+    bool plain = target;
     double total = 0.0;
     auto part = [&](int s) {
       if (s >= g.pieces) return 0.0;
@@ -374,22 +376,22 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     }
     const double goal = static_cast<double>(u) * total;
     double before = 0.0;
-    int slice = -1, last = 0;
+    int piece = -1, last = 0;
     double base = 0.0;
-    for (int s0 = 0; s0 < g.pieces && slice < 0; s0 += 64) {
+    for (int s0 = 0; s0 < g.pieces && piece < 0; s0 += 64) {
       const double v = part(s0 + lane), c = wave_scan(v) + before;
       const uint64_t some = __ballot(v > 0.0), over = __ballot(c > goal && v > 0.0);
       if (some) last = s0 + 63 - __builtin_clzll(some);
       if (over) {
         const int l = __builtin_ctzll(over);
-        slice = s0 + l;
+        piece = s0 + l;
         base = __shfl(c, l) - __shfl(v, l);
       }
       before = __shfl(c, 63);
     }
     if (lane == 0) {
-      sh_slice = slice >= 0 ? slice : last;  // (rounding: the last slice of any weight, to its end)
-      sh_goal = slice >= 0 ? goal - base : INFINITY;
+      sh_piece = piece >= 0 ? piece : last;  // (rounding: the last piece of any weight, to its end)
+      sh_goal = piece >= 0 ? goal - base : INFINITY;
       sh_plain = plain;
     }
   }
@@ -399,7 +401,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
     d.hot = -1;
   }
   // contiguous places to a thread
-  const int64_t i0 = static_cast<int64_t>(sh_slice) * kPiece + tid * kPer;
+  const int64_t i0 = static_cast<int64_t>(sh_piece) * kPiece + tid * kPer;
   const void* row = static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row;
   float v[kPer], q[kPer];
   load_row<DT, kPer>(row, i0, a.vocab, -INFINITY, v);
@@ -442,7 +444,7 @@ __device__ __forceinline__ int find_token(const VerifyArgs& g, int b, const Draw
 template <int DT>
 __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs g) {
   const qmv_verify_args& a = g.a;
-  const int first_slice = blockIdx.x * g.span, b = blockIdx.y, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int first_piece = blockIdx.x * g.span, b = blockIdx.y, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r0 = min(max(a.row_start[b], 0), static_cast<int>(a.rows));
   const int end = min(max(a.row_start[b + 1], r0), static_cast<int>(a.rows));
   const int n = min(end - r0, a.max_rows);
@@ -484,25 +486,26 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
   }
 
   // (n > 0 here has a row that draws: the last row is never accepted)
-  const bool draws = n > 0 && !greedy && rs.max > -INFINITY;
+  const bool draws = n > 0 && !greedy && rs.max > -INFINITY, rejected = at + 1 < n;
   int token = n > 0 && greedy && rs.max > -INFINITY ? rs.best : -1;
+  Draw d;
   if (draws) {
-    const bool rejected = at + 1 < n;
-    Draw d;
     d.row = r0 + at;
     d.max = rs.max;
     d.sum = rs.sum;
     d.c_t = c_t;
     d.q = rejected && a.draft_probs ? a.draft_probs + d.row * a.draft_row : nullptr;
     d.hot = rejected && !a.draft_probs ? a.tokens[d.row + 1] : -1;
-    // (no barrier between slices: the next one's loads run under this one's sums)
+  }
+  if (draws && rejected) {
+    // (no barrier between pieces: the next one's loads run under this one's sums)
     constexpr int kGroup = 4;
     __shared__ double sums[kGroup][kWaves];
-    const int last_slice = min(first_slice + g.span, g.pieces);
-    for (int s0 = first_slice; s0 < last_slice; s0 += kGroup) {
+    const int last_piece = min(first_piece + g.span, g.pieces);
+    for (int s0 = first_piece; s0 < last_piece; s0 += kGroup) {
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) {
-        if (s0 + k >= last_slice) break;
+        if (s0 + k >= last_piece) break;
         const int64_t i0 = static_cast<int64_t>(s0 + k) * kPiece;
         float v[kPer], q[kPer];
         load_pieces<DT, kThreads, kPer>(static_cast<const typename Logits<DT>::word*>(a.logits) + d.row * a.logits_row, i0,
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
         if (__lane_id() == 0) sums[k][wave] = s;
       }
       __syncthreads();
-      if (tid < min(kGroup, last_slice - s0)) {
+      if (tid < min(kGroup, last_piece - s0)) {
         double s = 0.0;
 #pragma unroll
         for (int k = 0; k < kWaves; ++k) s += sums[tid][k];
@@ -545,9 +548,11 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyArgs 
     }
     __syncthreads();
     if (!sh_last) return;
-    token = find_token<DT>(g, b, d, u);
-  } else if (first_slice != 0) {
+    token = find_token<DT>(g, b, d, u, false);
+  } else if (first_piece != 0) {
     return;
+  } else if (draws) {
+    token = find_token<DT>(g, b, d, u, true);
   }
   if (tid == 0) a.accepted[b] = n > 0 ? at : 0;
   for (int r = r0 + tid; r < end; r += kThreads)
