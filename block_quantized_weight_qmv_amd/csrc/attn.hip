@@ -722,14 +722,16 @@ struct Attn {
     f32x16 s[NT];
     float mx;
     const lds_u8* lk = (const lds_u8*)smem;
-    if (tiles) copy_k(0);
+    if (tiles) {
+      copy_k(0);
+      copy_v(0);
+      if (tiles > 1) copy_k(1);
+    }
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     t.arrived();
     wait_copies<0>();
     lds_barrier();
     if (tiles) {
-      copy_v(0);
-      if (tiles > 1) copy_k(1);
       t.template scores<NT>(lk, s);
       hide(0, s);
       if (t.template moves<NT>(s, mx)) t.move(mx);
@@ -1120,7 +1122,7 @@ constexpr double kStartUs = 4.0, kWideTileUs = 2.2, kNarrowTilesUs = 1.5;
 
 // How many ranges to cut `keys` into for each of `units` row tiles: the fewest
 // microseconds, by workgroups of `tile` microseconds for each `tile_keys`
-// keys, the parts' way through the workspace, written and read at 4 TB/s, and
+// keys, the parts' way through the workspace, written and read at 2 TB/s, and
 // `other` microseconds of other workgroups that fill the slots left free.
 static int64_t key_ranges(int64_t keys, int64_t units, int tile_keys, double tile, double part_bytes, double other) {
   const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
@@ -1131,7 +1133,7 @@ static int64_t key_ranges(int64_t keys, int64_t units, int tile_keys, double til
     const double each = kStartUs + tile * static_cast<double>((tiles + s - 1) / s);
     const double left = other - static_cast<double>(rounds * kResident - units * s) * each;
     const double us = static_cast<double>(rounds) * each + (left > 0 ? left / kResident + kStartUs * 2 : 0.0) +
-                      static_cast<double>(s) * part_bytes * 2 / 4e6;
+                      static_cast<double>(s) * part_bytes * 2 / 2e6;
     if (us < best) {
       best = us;
       n = s;
