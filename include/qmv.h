@@ -437,10 +437,13 @@ typedef struct qmv_attn_args {
  * sees no key gives zeros and lse = -inf.  A row outside every sequence sees
  * the prefix alone; a row past its sequence's max_rows is filled with NaN; a
  * suffix longer than max_suffix is cut there.
- * Scores, maxima, sums and outputs are held in fp32; the probabilities enter
+ * Scores, maxima, sums and outputs are held in fp32.  The probabilities enter
  * the second product as two values of q's type that together hold 16 bits or
- * more.  Keys are split over workgroups whose partial results (in the
+ * more -- except, over the prefix, where a key head has more than 64 rows
+ * (rows * heads / kv_heads): there they are rounded once to q's type, as the
+ * output is.  Keys are split over workgroups whose partial results (in the
  * workspace) are joined in a fixed order: results do not depend on timing.
+ * out must not overlap what the call reads.
  * Inference only: no gradient.
  * workspace as in qmv_gemv_multi_ws: 256-byte aligned, at least
  * qmv_attn_workspace_size bytes (QMV_ERR_SIZE), no initial value.  rows = 0
@@ -499,7 +502,7 @@ typedef struct qmv_verify_args {
  * fixed order: results do not depend on timing, and a draw differs from exact
  * arithmetic only within about 1e-12 of a border between two tokens.
  * Sequences of more than max_rows rows have the rows past it treated as not
- * there.  workspace as in qmv_attn.  rows = 0 launches nothing if nseq is 0
+ * there.  out_tokens and accepted must not overlap what the call reads.  workspace as in qmv_attn.  rows = 0 launches nothing if nseq is 0
  * too.  Errors: QMV_ERR_NULL, QMV_ERR_SHAPE (counts, row strides below
  * vocab), QMV_ERR_ALIGN, QMV_ERR_SIZE, QMV_ERR_UNSUPPORTED (dtype, vocab).
  * Enqueues only; legal inside HIP stream capture. */
