@@ -5,7 +5,7 @@
 //
 // One launch walks the keys, a second joins the parts.  The query heads that
 // share a key head, of all rows of the step, stand side by side as rows of one
-// matrix, so a prefix key is read once per 128 (wide) or 32 (narrow) of them
+// matrix, so a prefix key is read once per 128 (wide) or 32 or 16 (narrow) of them
 // and not once per sequence; a sequence's own keys meet its own rows only.
 // The keys of the prefix, and of long suffixes, are split over workgroups,
 // each of which keeps a running maximum and sum and leaves its unnormalized
@@ -19,14 +19,15 @@
 // operand: its k index runs over the keys in that same order, which V's
 // transposing LDS reads follow.  P never goes through LDS.
 //
-// Measured (28 query and 4 key heads of 128, bf16): 64 sequences of up to 8
-// rows on 32768 shared tokens and up to 1024 of their own, 137.6 GFLOP, 165 us
-// and 15 us to join, 780 TFLOP/s of the 1340 that a large matrix product
-// reaches: matrix and vector instructions (a probability costs seven) share a
-// wave's time, with the matrix pipes busy for about half of it.  32 sequences
-// of up to 2111 own tokens (12 heads of 80, fp16, 150 MB) 43 us and 5.4 us: by
-// the copies in flight, two workgroups of 64 KB a compute unit.  One row on 1000
-// tokens 5.8 us and 3 us: latencies in a row.
+// Measured (kernel times are the fastest of 40 traced).  64 sequences of up to
+// 8 rows on 32768 shared tokens and up to 1024 of their own (28 query and 4 key
+// heads of 128, bf16), 137.6 GFLOP: 177 us a call, 780 TFLOP/s, where a large
+// matrix product reaches 1340; 164 us and 15 us to join.  Counters: matrix
+// pipes busy for 40 % of the time, 6.9 vector instructions to a matrix
+// instruction.  32 sequences of up to 2111 own tokens (12 heads of 80, fp16,
+// 150 MB): 43 us and 5.3 us; waves wait for 42 % of their time, most likely
+// for copies, with two workgroups of 64 KB to a compute unit.  One row on 1000
+// tokens: 5.8 us and 3 us, latencies in a row.
 //
 // K and V tiles go from memory to LDS without passing registers.  16-byte
 // chunks of a tile's row are permuted by the row's number so that neither
@@ -191,8 +192,8 @@ __device__ __forceinline__ uint32_t round_pair(float x, float y, float& sum) {
 // output is off by little but its own rounding.  Where many rows share the
 // keys the products bound the kernel, and each probability is rounded once:
 // an output's error grows by the square root of 2 at most (independent
-// roundings of weights and of the output; 2.3e-3 against 1.7e-3 of the
-// outputs' norm in bf16), and 64 sequences of up to 8 rows on 32768 tokens
+// roundings of weights and of the output; in bf16 2.3e-3 of the outputs'
+// norm, where 1.7e-3 is what fp32 arithmetic rounded at the end leaves), and 64 sequences of up to 8 rows on 32768 tokens
 // took 195 us where the split took 227.  The sum takes the rounded
 // probabilities too, so that they stay a mean's weights.
 template <bool BF, int DP, bool SPLIT>

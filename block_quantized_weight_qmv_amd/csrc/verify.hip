@@ -12,10 +12,13 @@
 //
 // Exponentials and sums are in 64 bits.  A draw compares a running sum of up
 // to 2^24 probabilities with u times their total; in 32 bits their errors
-// would move about one draw in a hundred over 152064 flat probabilities to a
-// neighbouring token.  At eighteen 64-bit instructions of 8 clocks each, the
-// exponentials bound the first launch: 288 rows of 152064 fp32 logits take 47
-// us (their reads alone, 175 MB, 28 us at 6.3 TB/s).
+// would move, by estimate (152064 borders, an error of 2^-24 or so), about one
+// draw in a hundred over flat probabilities to a neighbouring token.  An
+// exponential takes some eighteen 64-bit instructions.  The first launch takes
+// 46 us (the fastest of 40) on 288 rows of 152064 fp32 logits, whose reads
+// alone, 175 MB, would take 25 at 7.08 TB/s: a SIMD issues a vector
+// instruction every 7.4 clocks, and its waves wait half of their time to issue
+// and 37 % for loads (counters).
 #include <algorithm>
 
 #include "device_util.h"
@@ -28,7 +31,7 @@ constexpr int kRowThreads = 256, kRowPer = 32, kPiece = 64 * kRowPer;
 // The second: a workgroup's slice, a piece again (one or, where there are
 // sequences enough to fill the chip, several of them).  Four 64-bit weights to
 // a thread: they are the longest step of a lone sequence (with 8192 tokens to
-// 1024 threads of one compute unit, 12.3 us against 8.6).
+// 1024 threads of one compute unit, 12.3 us against 8.6, the fastest of 40).
 constexpr int kThreads = 512, kWaves = kThreads / 64, kPer = 4;
 static_assert(kThreads * kPer == kPiece, "a slice is a piece");
 
