@@ -441,7 +441,8 @@ typedef struct qmv_attn_args {
  * the second product as two values of q's type that together hold 16 bits or
  * more -- except, over the prefix, where a key head has more than 64 rows
  * (rows * heads / kv_heads): there they are rounded once to q's type, as the
- * output is.  Keys are split over workgroups whose partial results (in the
+ * output is.  (fp16 holds no probability closer than 2^-37 of the largest that a
+ * row sees; its exponents take scores of magnitudes up to 2^24.)  Keys are split over workgroups whose partial results (in the
  * workspace) are joined in a fixed order: results do not depend on timing.
  * out must not overlap what the call reads.
  * Inference only: no gradient.
