@@ -139,12 +139,14 @@ __device__ __forceinline__ int swz(int row) {
 __device__ __forceinline__ void copy_to_lds(const void* src, uint32_t lds) {
   __asm__ __volatile__("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off"
                        :
-                       : "v"(src), "s"(lds));
+                       : "v"(src), "s"(lds)
+                       : "m0");
 }
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
   __asm__ __volatile__("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
                        :
-                       : "v"(off), "s"(base), "s"(lds));
+                       : "v"(off), "s"(base), "s"(lds)
+                       : "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {  // all but the last N
