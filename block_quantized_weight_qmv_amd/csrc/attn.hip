@@ -78,6 +78,7 @@ struct KeySource {
   int64_t row;            // bytes from one token to the next (within a page)
   int64_t page;           // bytes from one page to the next
   int shift, npages;      // log2 of the page size
+  int dim;                // D
 };
 
 // n / d for 0 <= n < 2^31, as a multiplication (Granlund and Montgomery,
@@ -130,23 +131,27 @@ __device__ __forceinline__ int swz(int row) {
   return DP == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
 }
 
-// 64 lanes x 16 bytes from memory to LDS at `lds` (+ 16 x lane).  The s_nop
-// covers an M0 or address written just before, which the compiler cannot see
+// 16 bytes of each lane of `lanes` from memory to LDS at `lds` + 16 x lane.  The
+// s_nop covers an M0 or address written just before, which the compiler cannot see
 // being used here.  LDS accesses are kept apart from copies by the waits and
 // barriers between them (wait_copies, wait_lds, lds_barrier, which no memory
 // access crosses); so that copies may run among reads of other tiles, they
 // themselves are no such border.
-__device__ __forceinline__ void copy_to_lds(const void* src, uint32_t lds) {
-  __asm__ __volatile__("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off"
-                       :
-                       : "v"(src), "s"(lds)
-                       : "m0");
+__device__ __forceinline__ void copy_to_lds(const void* src, uint32_t lds, uint64_t lanes) {
+  uint64_t all;
+  __asm__ __volatile__(
+      "s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, %0"
+      : "=&s"(all)
+      : "v"(src), "s"(lds), "s"(lanes)
+      : "m0", "scc");
 }
-__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
-  __asm__ __volatile__("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
-                       :
-                       : "v"(off), "s"(base), "s"(lds)
-                       : "m0");
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds, uint64_t lanes) {
+  uint64_t all;
+  __asm__ __volatile__(
+      "s_mov_b32 m0, %3\n\ts_and_saveexec_b64 %0, %4\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, %0"
+      : "=&s"(all)
+      : "v"(off), "s"(base), "s"(lds), "s"(lanes)
+      : "m0", "scc");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {  // all but the last N
@@ -579,16 +584,27 @@ template <int DP, int NI>
 struct TileCopy {
   static constexpr int CPR = DP / 8, RPI = 64 / CPR;
   static constexpr int NV = 16 / RPI;  // instructions until the permutation repeats
-  uint32_t off[NV];  // this lane's bytes from the instruction's first row
+  static constexpr int NM = NV < NI ? NV : NI;
+  uint32_t off[NV];    // this lane's bytes from the instruction's first row
+  uint64_t lanes[NM];  // those whose chunk lies before column D
 
-  __device__ __forceinline__ static int chunk(int row, int lane, int D) {
-    const int ch = (lane % CPR) ^ swz<DP>(row);
-    return ch * 8 < D ? ch : 0;  // (columns past D: anything of the row; they meet zeros of q, or are not stored)
-  }
+  __device__ __forceinline__ static int chunk(int row, int lane) { return (lane % CPR) ^ swz<DP>(row); }
   __device__ __forceinline__ void init(const KeySource& src, int row0, int lane, int D) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + chunk(row0 + i * RPI + lane / CPR, lane, D) * 16;
+    for (int i = 0; i < NV; ++i) {
+      const int ch = chunk(row0 + i * RPI + lane / CPR, lane);
+      off[i] = static_cast<uint32_t>(lane / CPR * static_cast<uint32_t>(src.row)) + ch * 16;
+      if (i < NM) lanes[i] = __ballot(ch * 8 < D);
+    }
+  }
+  // The columns from D on, which no copy fills, in this wave's rows of a tile
+  // whose row row0 is at `at`: zeros, which the zeros of q meet.
+  __device__ __forceinline__ static void clear_past(lds_u8* at, int row0, int lane, int D) {
+    constexpr int kRows = NI * RPI;
+    const u32x4 z = {0, 0, 0, 0};
+    const int r = lane % kRows;
+    for (int ch = D / 8 + lane / kRows; ch < CPR; ch += 64 / kRows)
+      *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at + r * DP * 2 + (ch ^ swz<DP>(row0 + r)) * 16) = z;
   }
   // Lane r: where tile row row0 + r begins; an instruction takes its first row's.
   __device__ __forceinline__ static uint64_t starts(const KeySource& src, const uint8_t* base, const int* pages, int first,
@@ -617,8 +633,8 @@ struct TileCopy {
     }
   }
   // Instruction i of a tile whose row row0 is at `lds`.
-  __device__ __forceinline__ static void one(uint64_t from, uint32_t o, int i, uint32_t lds) {
-    copy_to_lds(start(from, i), o, lds + i * RPI * DP * 2);
+  __device__ __forceinline__ void one(uint64_t from, uint32_t o, int i, uint32_t lds) const {
+    copy_to_lds(start(from, i), o, lds + i * RPI * DP * 2, lanes[i % NM]);
   }
 
   // Key key0 is the tile's row 0.  Rows past the last key before `end` repeat
@@ -626,7 +642,7 @@ struct TileCopy {
   // used.  each: every instruction's rows lie in one page of the pool (or
   // tokens are contiguous) and `off` holds.
   __device__ __forceinline__ void copy(const KeySource& src, const uint8_t* base, const int* pages, int first, bool each,
-                                       int key0, int end, int row0, uint32_t lds, int lane, int D) const {
+                                       int key0, int end, int row0, uint32_t lds, int lane) const {
     const int in_page = (1 << src.shift) - 1;
     if (each) {
       const uint64_t from = starts(src, base, pages, first, key0, end, row0, lane);
@@ -640,7 +656,9 @@ struct TileCopy {
     for (int i = 0; i < NI; ++i) {
       const int row = row0 + i * RPI + lane / CPR, key = min(key0 + row, end - 1);
       const int64_t page = pages ? max(pages[(key >> src.shift) - first], 0) : 0, in = pages ? key & in_page : key;
-      copy_to_lds(base + page * src.page + in * src.row + chunk(row, lane, D) * 16, lds + (row0 + i * RPI) * DP * 2);
+      const int64_t at = page * src.page + in * src.row;
+      const int ch = chunk(row, lane);
+      copy_to_lds(base + at + ch * 16, lds + (row0 + i * RPI) * DP * 2, __ballot(ch * 8 < src.dim));
     }
   }
 };
@@ -709,10 +727,10 @@ struct Attn {
     const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + kWideKeys - 1) / kWideKeys;
     // K of tile i in buffer i & 1, V in the two after them
     auto copy_k = [&](int tile) {
-      cp.copy(src, src.k, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (tile & 1) * kTileBytes, lane, D);
+      cp.copy(src, src.k, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (tile & 1) * kTileBytes, lane);
     };
     auto copy_v = [&](int tile) {
-      cp.copy(src, src.v, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (2 + (tile & 1)) * kTileBytes, lane, D);
+      cp.copy(src, src.v, pg, first, true, k0 + tile * kWideKeys, k1, row0, lds + (2 + (tile & 1)) * kTileBytes, lane);
     };
     auto partial = [&](int tile) { return bad || k1 - k0 - tile * kWideKeys < kWideKeys; };
     auto hide = [&](int tile, f32x16* s) {
@@ -750,6 +768,8 @@ struct Attn {
       copy_v(0);
       if (tiles > 1) copy_k(1);
     }
+    if (D < DP)
+      for (int i = 0; i < 4; ++i) cp.clear_past((lds_u8*)smem + i * kTileBytes + row0 * ROWB, row0, lane, D);
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
     t.arrived();
     wait_copies<0>();
@@ -844,8 +864,12 @@ struct Attn {
     const uint32_t klds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(kt)), vlds = klds + kWaveBytes;
     const int tiles = src.table && src.npages == 0 ? 0 : (k1 - k0 + 31) / 32;
     if (wave < tiles) {
-      cp.copy(src, src.k, pg, first, each, k0 + wave * 32, k1, 0, klds, lane, D);
-      cp.copy(src, src.v, pg, first, each, k0 + wave * 32, k1, 0, vlds, lane, D);
+      cp.copy(src, src.k, pg, first, each, k0 + wave * 32, k1, 0, klds, lane);
+      cp.copy(src, src.v, pg, first, each, k0 + wave * 32, k1, 0, vlds, lane);
+      if (D < DP) {
+        cp.clear_past(kt, 0, lane, D);
+        cp.clear_past(vt, 0, lane, D);
+      }
     }
     Tile t;
     t.init(static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head, D, a.scale, lane);
@@ -860,7 +884,7 @@ struct Attn {
       wait_copies<NI>();  // outstanding: this tile's K, its V
       t.keys(kt, s);
       wait_lds();
-      if (more) cp.copy(src, src.k, pg, first, each, key0 + 128, k1, 0, klds, lane, D);
+      if (more) cp.copy(src, src.k, pg, first, each, key0 + 128, k1, 0, klds, lane);
       const bool partly = key0 + 32 > min(draft0, k1) || bad;  // some rows do not see some of the keys
       if (partly) {
         // bit j: the lane's row sees key key0 + j
@@ -883,7 +907,7 @@ struct Attn {
       if (partly) unseen_values(t, s, vt, lane, bad ? 0 : min(draft0, k1) - key0);
       t.product(vt, p);
       wait_lds();
-      if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane, D);
+      if (more) cp.copy(src, src.v, pg, first, each, key0 + 128, k1, 0, vlds, lane);
     }
     __syncthreads();
 
@@ -935,7 +959,7 @@ struct Attn {
   static __device__ __forceinline__ void unseen_values(Tile& t, const typename Tile::Keys& s, lds_u8* vt, int lane,
                                                        int from) {
     const int r = lane & 31;
-    constexpr uint16_t kExp = BF ? 0x7F80u : 0x7C00u;  // (columns past D, where D is not DP, are some of the row's)
+    constexpr uint16_t kExp = BF ? 0x7F80u : 0x7C00u;
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     u32x4 w[CPR / 2];
 #pragma unroll
@@ -972,6 +996,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) attn_parts_kernel(cons
   int shift = 31 - __builtin_clz(a.page_size > 0 ? a.page_size : 1);
   src.shift = shift;
   src.npages = static_cast<int>(a.num_pages);
+  src.dim = a.head_dim;
   src.page = a.page_stride * 2;
   int id = blockIdx.x;
   const int before = static_cast<int>(g.p.suffix_first ? g.p.suffix_wgs : g.p.prefix_wgs);
