@@ -433,7 +433,11 @@ typedef struct qmv_attn_args {
  * set: a draft tree; max_rows <= 64).  The prefix is read once for all rows of
  * a key head together, not once per sequence.  A key on a page number outside
  * [0, num_pages) is not seen.  What no row sees (stale tokens of a page, the
- * keys above) may hold anything, infinities and NaN among them.  A row that
+ * keys above) may hold anything, infinities and NaN among them.  Infinities in
+ * what a row sees count as fp32 arithmetic has them: a score of -inf weighs nothing,
+ * one of +inf makes the row NaN, and an infinite value is that infinity in its
+ * column, unless its weight is 0 or both signs meet (a row whose scores are finite
+ * and whose output is not takes up to 250 times as long).  A row that
  * sees no key gives zeros and lse = -inf.  A row outside every sequence sees
  * the prefix alone; a row past its sequence's max_rows is filled with NaN; a
  * suffix longer than max_suffix is cut there.
