@@ -392,30 +392,35 @@ embed_kernel(const uint8_t* w, uint64_t scales_offset, int rows, int cols, const
   }
 }
 
+template <int FMT, int OUT>
+static hipError_t embed_typed(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out,
+                              hipStream_t s) {
+  const int rows = static_cast<int>(W.rows), cols = static_cast<int>(W.cols);
+  const int chunks = cols / 16, per = chunks < 256 ? 256 / chunks : 1, pieces = (chunks + 255) / 256;
+  // A launch's work-items along x are counted in 32 bits (2^32 of them and more
+  // wrap around, with no error): more rows than that take several launches.
+  const int64_t most = (int64_t{1} << 23) * per;
+  for (int64_t i = 0; i < n; i += most) {
+    const int64_t k = n - i < most ? n - i : most;
+    const dim3 grid(static_cast<unsigned>((k + per - 1) / per), pieces < 65535 ? pieces : 65535);
+    hipLaunchKernelGGL((embed_kernel<FMT, OUT>), grid, dim3(256), 0, s, static_cast<const uint8_t*>(W.data),
+                       W.scales_offset, rows, cols, ids + i, k, scale,
+                       static_cast<uint8_t*>(out) + i * cols * (OUT == QMV_F32 ? 4 : 2));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int FMT>
 static hipError_t embed_fmt(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
                             hipStream_t s) {
-  const int rows = static_cast<int>(W.rows), cols = static_cast<int>(W.cols);
-  const int chunks = cols / 16, per = chunks < 256 ? 256 / chunks : 1, pieces = (chunks + 255) / 256;
-  const dim3 grid(static_cast<unsigned>((n + per - 1) / per), pieces < 65535 ? pieces : 65535);
-  const uint8_t* w = static_cast<const uint8_t*>(W.data);
   switch (out_dtype) {
-    case QMV_F32:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F32>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
-                         scale, out);
-      break;
-    case QMV_F16:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_F16>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
-                         scale, out);
-      break;
-    case QMV_BF16:
-      hipLaunchKernelGGL((embed_kernel<FMT, QMV_BF16>), grid, dim3(256), 0, s, w, W.scales_offset, rows, cols, ids, n,
-                         scale, out);
-      break;
-    default:
-      return hipErrorInvalidValue;
+    case QMV_F32: return embed_typed<FMT, QMV_F32>(W, ids, n, scale, out, s);
+    case QMV_F16: return embed_typed<FMT, QMV_F16>(W, ids, n, scale, out, s);
+    case QMV_BF16: return embed_typed<FMT, QMV_BF16>(W, ids, n, scale, out, s);
+    default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
 }
 
 hipError_t embed(const qmv_weights& W, const int32_t* ids, int64_t n, float scale, void* out, int out_dtype,
