@@ -1330,7 +1330,7 @@ static AttnPlan plan_attn(const qmv_attn_args& a) {
 
 bool attn_fits(const qmv_attn_args& a) {
   const AttnPlan p = plan_attn(a);
-  return p.prefix_wgs + p.suffix_wgs <= INT32_MAX;
+  return p.prefix_wgs + p.suffix_wgs <= UINT32_MAX / 256;  // (a launch of 2^32 work-items and more wraps around, with no error)
 }
 
 static size_t ml_bytes(const qmv_attn_args& a, const AttnPlan& p) {
