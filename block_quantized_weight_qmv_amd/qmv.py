@@ -458,12 +458,19 @@ def _check_one_device(pairs) -> None:
         raise QmvError(-6, f"{', '.join(n for n, t in pairs if t is not None)}: tensors on {sorted(devices)}")
 
 
+def _check_with(what: str, t, name: str, u) -> None:
+    """t on the device of u (integer addresses pass)."""
+    if hasattr(t, "device") and hasattr(u, "device") and t.device != u.device:
+        raise QmvError(-6, f"{what} on {t.device}, {name} on {u.device}")
+
+
 def qmv_embed(W: QmvWeights, ids, n: int, out, out_dtype, scale: float = 1.0, stream=None) -> None:
     """out[i] = scale * W[ids[i]] for n int32 device ids; ids outside the table give rows of zeros."""
     od = _dtype(out_dtype)
     if n > 0:
         _check_vec(ids, "ids", _I32, n)
         _check_dev(out, "out", od, n * W.cols)
+        _check_with("ids", ids, "out", out)
     _check(lib().qmv_embed(ctypes.byref(W), _ptr(ids), n, scale, _ptr(out), od, _stream(stream, out)))
 
 
@@ -558,11 +565,12 @@ def qmv_attn_workspace_size(a: QmvAttnArgs) -> int:
 
 def qmv_attn(a: QmvAttnArgs, workspace, workspace_bytes: int, stream=None) -> None:
     """Attention of the step's rows (qmv_create_attn) over the shared prefix and their sequences' suffixes."""
+    owner = getattr(a, "owner", None)
+    q = owner["q"] if owner else None
     if workspace is not None:
         _check_dev(workspace, "workspace", None, workspace_bytes)
-    owner = getattr(a, "owner", None)
-    _check(lib().qmv_attn(ctypes.byref(a), _ptr(workspace), workspace_bytes,
-                          _stream(stream, owner["q"] if owner else None, workspace)))
+        _check_with("workspace", workspace, "q", q)
+    _check(lib().qmv_attn(ctypes.byref(a), _ptr(workspace), workspace_bytes, _stream(stream, q, workspace)))
 
 
 def qmv_create_verify(logits, tokens, row_start, max_rows: int, u_accept, u_sample, out_tokens, accepted, *,
@@ -611,11 +619,12 @@ def qmv_verify_workspace_size(a: QmvVerifyArgs) -> int:
 
 def qmv_verify(a: QmvVerifyArgs, workspace, workspace_bytes: int, stream=None) -> None:
     """Drafted tokens checked against the target's probabilities (qmv_create_verify)."""
+    owner = getattr(a, "owner", None)
+    logits = owner["logits"] if owner else None
     if workspace is not None:
         _check_dev(workspace, "workspace", None, workspace_bytes)
-    owner = getattr(a, "owner", None)
-    _check(lib().qmv_verify(ctypes.byref(a), _ptr(workspace), workspace_bytes,
-                            _stream(stream, owner["logits"] if owner else None, workspace)))
+        _check_with("workspace", workspace, "logits", logits)
+    _check(lib().qmv_verify(ctypes.byref(a), _ptr(workspace), workspace_bytes, _stream(stream, logits, workspace)))
 
 
 def qmv_probe_read_outputs(nbytes: int) -> int:
