@@ -21,11 +21,11 @@
 //
 // Measured (kernel times are the fastest of 40 traced).  64 sequences of up to
 // 8 rows on 32768 shared tokens and up to 1024 of their own (28 query and 4 key
-// heads of 128, bf16), 137.6 GFLOP: 177 us a call, 780 TFLOP/s, where a large
-// matrix product reaches 1340; 164 us and 15 us to join.  Counters: matrix
-// pipes busy for 40 % of the time, 6.9 vector instructions to a matrix
+// heads of 128, bf16), 137.6 GFLOP: 176 us a call, 780 TFLOP/s, where a large
+// matrix product reaches 1340; 167 us and 16 us to join.  Counters: matrix
+// pipes busy for 39 % of the time, 6.8 vector instructions to a matrix
 // instruction.  32 sequences of up to 2111 own tokens (12 heads of 80, fp16,
-// 150 MB): 43 us and 5.3 us; waves wait for 42 % of their time, most likely
+// 150 MB): 43 us and 5.1 us; waves wait for 40 % of their time, most likely
 // for copies, with two workgroups of 64 KB to a compute unit.  One row on 1000
 // tokens: 5.8 us and 3 us, latencies in a row.
 //
@@ -1297,6 +1297,7 @@ static AttnPlan plan_attn(const qmv_attn_args& a) {
   const int64_t near = int64_t{1} << 27;  // elements
   const bool pages_fit = a.page_size >= rpi && a.page_row < near;
   p.each = pages_fit;
+  // (112 rows: wide tiles take 30 us on 32768 tokens, narrow ones 43; on 1024 tokens 13.0 and 12.1)
   p.wide = M > 64 && (a.prefix_pages ? pages_fit : a.prefix_row < near);
   const int64_t suffix_rows = std::min<int64_t>(a.max_rows, a.rows) * p.groups;
   p.rows = suffix_rows <= 16 && (p.wide || M <= 16 || a.prefix_len == 0) ? 16 : 32;
@@ -1361,7 +1362,8 @@ static hipError_t attn_typed(const AttnKernelArgs& g, hipStream_t s) {
                        : D <= 128 ? parts(std::integral_constant<int, 128>{})
                                   : parts(std::integral_constant<int, 256>{});
   if (e != hipSuccess) return e;
-  // Few rows of many parts: four waves to a row.
+  // Few rows of many parts: four waves to a row (5 draft trees take 13.1 us a
+  // call, with one wave 17.1; 256 x 1 rows of few parts 44, with four waves 53).
   const int64_t all = g.a.rows * g.a.heads;
   if (all <= 8192 && g.p.psplits + g.p.ssplits >= 8) {
     const dim3 grid(static_cast<unsigned>(all));

@@ -11,7 +11,7 @@ tokens drafted after it -- through
     qmv_attn         each row over the shared prompt and its own sequence's pages
     qmv_verify       drafts accepted or a token drawn, from given random numbers
 
-and nothing but the accepted counts returns to the host.  (Norms, SiLU and the cache's writes are torch operations
+and nothing but the step's tokens and the accepted counts returns to the host.  (Norms, SiLU and the cache's writes are torch operations
 here.)  It first decodes one token a step, then verifies those very tokens as drafts, several a step, and says how many
 steps that saved.
 """

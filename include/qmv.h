@@ -440,14 +440,21 @@ typedef struct qmv_attn_args {
  * and whose output is not takes up to 250 times as long).  A row that
  * sees no key gives zeros and lse = -inf.  A row outside every sequence sees
  * the prefix alone; a row past its sequence's max_rows is filled with NaN; a
- * suffix longer than max_suffix is cut there.
+ * suffix_len above max_suffix counts as max_suffix, the sequence's rows as the
+ * last of those tokens.  max_suffix may be a capacity: it changes the order of
+ * sums only, but the key ranges are planned for suffixes of that length, and a
+ * call whose suffixes are far shorter takes longer than with their own maximum.
+ * Rows are meant to be few for each sequence, as drafts are: 16 or 32 (row, query
+ * head) pairs of a key head together walk all of their sequence's keys, a
+ * prompt's rows too.
  * Scores, maxima, sums and outputs are held in fp32.  The probabilities enter
  * the second product as two values of q's type that together hold 16 bits or
  * more -- except, over the prefix, where a key head has more than 64 rows
  * (rows * heads / kv_heads): there they are rounded once to q's type, as the
  * output is.  (fp16 holds no probability closer than 2^-37 of the largest that a
- * row sees; its exponents take scores of magnitudes up to 2^24.)  Keys are split over workgroups whose partial results (in the
- * workspace) are joined in a fixed order: results do not depend on timing.
+ * row sees; its exponents take scores of magnitudes up to 2^24.)  Keys are split
+ * over workgroups whose partial results (in the workspace) are joined in a fixed
+ * order: results do not depend on timing.
  * out must not overlap what the call reads.
  * Inference only: no gradient.
  * workspace as in qmv_gemv_multi_ws: 256-byte aligned, at least
@@ -507,8 +514,8 @@ typedef struct qmv_verify_args {
  * fixed order: results do not depend on timing, and a draw differs from exact
  * arithmetic only within about 1e-12 of a border between two tokens.
  * Sequences of more than max_rows rows have the rows past it treated as not
- * there.  out_tokens and accepted must not overlap what the call reads.  workspace as in qmv_attn.  rows = 0 launches nothing if nseq is 0
- * too.  Errors: QMV_ERR_NULL, QMV_ERR_SHAPE (counts, row strides below
+ * there.  out_tokens and accepted must not overlap what the call reads.
+ * workspace as in qmv_attn.  rows = 0 launches nothing if nseq is 0 too.  Errors: QMV_ERR_NULL, QMV_ERR_SHAPE (counts, row strides below
  * vocab), QMV_ERR_ALIGN, QMV_ERR_SIZE, QMV_ERR_UNSUPPORTED (dtype, vocab).
  * Enqueues only; legal inside HIP stream capture. */
 int32_t qmv_verify_workspace_size(const qmv_verify_args* a, uint64_t* bytes);
