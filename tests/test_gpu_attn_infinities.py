@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from block_quantized_weight_qmv_amd import qmv
 from gpu_util import DEV, say
 from test_gpu_attn import Step
 
@@ -137,3 +138,42 @@ def test_large_finite_values_stay_finite():
                 x[x.isfinite()] = 1.5e38
             s.run()
             s.check()
+
+
+def test_infinities_where_rows_and_sequences_are_few_many_or_none():
+    for seqs in (5, 70):  # (fewer than 64 sequences are looked up at once)
+        rows = [(0, 2, 1, 3)[i % 4] for i in range(seqs)]
+        s = Step("f16", 4, 2, 72, 40, rows, [(0, 9, 1, 3)[i % 4] for i in range(seqs)], page=8, outside=2, seed=seqs)
+        s.vp[11, :, 4] = -INF
+        s.run()
+        assert bool((check_but(s, 4) == -INF).all())
+
+
+def test_infinities_without_a_prefix():
+    # three rows, two of their tokens cached: the first row sees nothing
+    s = Step("bf16", 4, 2, 64, 0, [3, 4], [2, 30], page=8, seed=7)
+    s.v_pages[int(s.table[0, 0]), 0, :, 6] = INF
+    s.v_pages[int(s.table[1, 3]), 5, :, 6] = -INF  # its last row's own
+    s.run()
+    got = check_but(s, 6)
+    assert bool((got[0] == 0).all()) and bool((got[1:3] == INF).all())
+    assert bool(got[3:6].isfinite().all()) and bool((got[6] == -INF).all())
+
+
+def test_infinities_in_a_captured_call():
+    s = Step("bf16", 14, 2, 128, 2000, [8] * 12, [38] * 12, seed=8)
+    s.vp[1000, :, 3] = INF
+    want, lse = s.run().clone(), s.lse.clone()
+    assert bool((want[..., 3] == INF).all())
+    a = s.args()
+    nws = qmv.qmv_attn_workspace_size(a)
+    ws, st, g = torch.empty(nws, dtype=torch.uint8, device=DEV), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        qmv.qmv_attn(a, ws, nws, st)
+    for _ in range(4):
+        s.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, want) and torch.equal(s.lse, lse)
+        assert torch.equal(s.run(), want)
