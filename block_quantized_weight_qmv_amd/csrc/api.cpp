@@ -68,9 +68,13 @@ static int64_t gemv_max_cols(int32_t fmt) {
     case QMV_Q6_K: return 16 * 16 * 256;
     case QMV_Q5_K: return 16 * 16 * 256;
     case QMV_INT4_G128: return 16 * 64 * 64;
+    case QMV_MXFP4: return 16 * 64 * 64;
     default: return 0;
   }
 }
+
+// Formats of a plane of 4-bit codes with a plane of scales behind it.
+static bool codes_plane(int32_t fmt) { return fmt == QMV_INT4_G128 || fmt == QMV_MXFP4; }
 
 static int32_t check_weights(const qmv_weights* W) {
   if (!W) return fail(QMV_ERR_NULL, "weights descriptor is NULL");
@@ -89,8 +93,8 @@ static int32_t check_weights(const qmv_weights* W) {
   if (W->nbytes != need)
     return fail(QMV_ERR_SIZE, "weights hold %llu bytes, format needs %llu",
                 (unsigned long long)W->nbytes, (unsigned long long)need);
-  const uint64_t soff = W->fmt == QMV_INT4_G128 ? static_cast<uint64_t>(W->rows * W->cols / 2)
-                        : planes                ? q4k_planes(W->rows, W->cols).a  // same unit for Q5_K, Q6_K
+  const uint64_t soff = codes_plane(W->fmt) ? static_cast<uint64_t>(W->rows * W->cols / 2)
+                        : planes            ? q4k_planes(W->rows, W->cols).a  // same unit for Q5_K, Q6_K
                                                 : 0;
   if (W->scales_offset != soff)
     return fail(QMV_ERR_FORMAT, "scales_offset %llu, expected %llu",
@@ -201,6 +205,123 @@ static int32_t check_verify(const qmv_verify_args* a) {
   return QMV_OK;
 }
 
+static bool is_dtype(int32_t d) { return d == QMV_F32 || d == QMV_F16 || d == QMV_BF16; }
+static int64_t size_of(int32_t dtype) { return dtype == QMV_F32 ? 4 : 2; }
+
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + static_cast<uintptr_t>(b_bytes) && b0 < a0 + static_cast<uintptr_t>(a_bytes);
+}
+
+static int32_t check_quantize(const qmv_weights* W, const void* x, int32_t x_dtype, int64_t x_row) {
+  const int32_t st = check_weights(W);
+  if (st != QMV_OK) return st;
+  if (W->fmt != QMV_MXFP4) return fail(QMV_ERR_UNSUPPORTED, "format %d is not quantized on the device", W->fmt);
+  if (!is_dtype(x_dtype)) return fail(QMV_ERR_UNSUPPORTED, "x dtype %d", x_dtype);
+  if (!x) return fail(QMV_ERR_NULL, "x is NULL");
+  if (!aligned16(x)) return fail(QMV_ERR_ALIGN, "x not 16-byte aligned");
+  if (x_row < W->cols || x_row % 8 || x_row > (int64_t{1} << 31))
+    return fail(QMV_ERR_SHAPE, "x_row %lld (a multiple of 8 from %lld to 2^31)", (long long)x_row, (long long)W->cols);
+  if (overlap(x, ((W->rows - 1) * x_row + W->cols) * size_of(x_dtype), W->data, static_cast<int64_t>(W->nbytes)))
+    return fail(QMV_ERR_SHAPE, "x overlaps W's bytes");
+  return QMV_OK;
+}
+
+static int32_t check_mx4(const qmv_mx4_args* a) {
+  if (!a) return fail(QMV_ERR_NULL, "arguments are NULL");
+  if (!is_dtype(a->y_dtype)) return fail(QMV_ERR_UNSUPPORTED, "y dtype %d", a->y_dtype);
+  if (a->epilogue != QMV_MX4_PLAIN && a->epilogue != QMV_MX4_SWIGLU)
+    return fail(QMV_ERR_UNSUPPORTED, "epilogue %d", a->epilogue);
+  if (a->rows < 0 || a->experts < 0)
+    return fail(QMV_ERR_SHAPE, "rows %lld or experts %d < 0", (long long)a->rows, a->experts);
+  if (a->rows > (int64_t{1} << 22) || a->experts > (1 << 16))
+    return fail(QMV_ERR_UNSUPPORTED, "rows %lld above 2^22 or experts %d above 2^16", (long long)a->rows, a->experts);
+  if (a->rows == 0) return QMV_OK;
+  for (const qmv_weights* W : {a->W, a->X}) {
+    const int32_t st = check_weights(W);
+    if (st != QMV_OK) return st;
+    if (W->fmt != QMV_MXFP4) return fail(QMV_ERR_FORMAT, "%s has format %d, not MXFP4", W == a->W ? "W" : "X", W->fmt);
+  }
+  if (a->W->cols != a->X->cols)
+    return fail(QMV_ERR_SHAPE, "W has %lld columns, X %lld", (long long)a->W->cols, (long long)a->X->cols);
+  const int64_t parts = static_cast<int64_t>(a->experts ? a->experts : 1) * (a->epilogue == QMV_MX4_SWIGLU ? 2 : 1);
+  if (a->W->rows % parts)
+    return fail(QMV_ERR_SHAPE, "W's %lld rows are not %lld equal parts", (long long)a->W->rows, (long long)parts);
+  if (a->experts && !a->expert_start) return fail(QMV_ERR_NULL, "expert_start is NULL");
+  if (!a->experts && a->expert_start) return fail(QMV_ERR_SHAPE, "expert_start without experts");
+  if (!a->x_index && a->X->rows < a->rows)
+    return fail(QMV_ERR_SHAPE, "X has %lld rows, y %lld", (long long)a->X->rows, (long long)a->rows);
+  if (!a->y) return fail(QMV_ERR_NULL, "y is NULL");
+  const int64_t n = a->W->rows / parts;
+  if (n > (int64_t{1} << 26)) return fail(QMV_ERR_UNSUPPORTED, "%lld outputs of a matrix, above 2^26", (long long)n);
+  if (a->y_row < n || a->y_row > (int64_t{1} << 31))
+    return fail(QMV_ERR_SHAPE, "y_row %lld (from %lld to 2^31)", (long long)a->y_row, (long long)n);
+  if (!aligned_to(a->y, size_of(a->y_dtype))) return fail(QMV_ERR_ALIGN, "y not aligned to its type");
+  if (!aligned_to(a->expert_start, 4) || !aligned_to(a->x_index, 4))
+    return fail(QMV_ERR_ALIGN, "expert_start or x_index not 4-byte aligned");
+  const int64_t bytes = ((a->rows - 1) * a->y_row + n) * size_of(a->y_dtype);
+  for (const qmv_weights* W : {a->W, a->X})
+    if (overlap(a->y, bytes, W->data, static_cast<int64_t>(W->nbytes)))
+      return fail(QMV_ERR_SHAPE, "y overlaps %s", W == a->W ? "W" : "X");
+  if (!mx4_gemm_fits(*a)) return fail(QMV_ERR_UNSUPPORTED, "more tiles than a launch has workgroups");
+  return QMV_OK;
+}
+
+static int32_t check_norm(const qmv_norm_args* a) {
+  if (!a) return fail(QMV_ERR_NULL, "arguments are NULL");
+  if (!is_dtype(a->dtype) || !is_dtype(a->weight_dtype) || !is_dtype(a->y_dtype))
+    return fail(QMV_ERR_UNSUPPORTED, "dtype %d, weight_dtype %d or y_dtype %d", a->dtype, a->weight_dtype, a->y_dtype);
+  for (const int32_t k : {a->pre, a->post})
+    if (k != QMV_NORM_NONE && k != QMV_NORM_RMS && k != QMV_NORM_LAYER) return fail(QMV_ERR_UNSUPPORTED, "norm %d", k);
+  if (a->rows < 0 || a->cols < 1)
+    return fail(QMV_ERR_SHAPE, "rows %lld < 0 or cols %lld < 1", (long long)a->rows, (long long)a->cols);
+  if (a->rows > INT32_MAX || a->cols > 32768)
+    return fail(QMV_ERR_UNSUPPORTED, "rows %lld above 2^31 or cols %lld above 32768", (long long)a->rows,
+                (long long)a->cols);
+  if (!(a->eps >= 0.f) || isinf(a->eps) || !isfinite(a->scale))
+    return fail(QMV_ERR_RANGE, "eps %g is not >= 0 and finite, or scale %g not finite", a->eps, a->scale);
+  if (a->rows == 0) return QMV_OK;
+  if (!a->residual || (!a->sum && !a->y)) return fail(QMV_ERR_NULL, "residual, or sum and y, are NULL");
+  if (!a->block && (a->gate || a->post != QMV_NORM_NONE)) return fail(QMV_ERR_SHAPE, "gate or post without block");
+  if ((a->post == QMV_NORM_NONE && (a->post_weight || a->post_bias)) ||
+      (a->pre == QMV_NORM_NONE && (a->pre_weight || a->pre_bias)))
+    return fail(QMV_ERR_SHAPE, "weight or bias without its norm");
+  if (!a->y && a->pre != QMV_NORM_NONE) return fail(QMV_ERR_SHAPE, "pre without y");
+  const struct {
+    const void* p;
+    int64_t row;
+    int32_t dtype;
+  } rows[] = {{a->residual, a->residual_row, a->dtype}, {a->block, a->block_row, a->dtype},
+              {a->gate, a->gate_row ? a->gate_row : a->cols, a->dtype}, {a->sum, a->sum_row, a->dtype},
+              {a->y, a->y_row, a->y_dtype}};
+  for (const auto& r : rows) {
+    if (!r.p) continue;
+    if (r.row < a->cols || r.row > (int64_t{1} << 31))
+      return fail(QMV_ERR_SHAPE, "row stride %lld (from cols %lld to 2^31)", (long long)r.row, (long long)a->cols);
+    if (!aligned_to(r.p, size_of(r.dtype))) return fail(QMV_ERR_ALIGN, "a pointer is not aligned to its type");
+  }
+  for (const void* p : {a->pre_weight, a->pre_bias, a->post_weight, a->post_bias})
+    if (!aligned_to(p, size_of(a->weight_dtype))) return fail(QMV_ERR_ALIGN, "a pointer is not aligned to its type");
+  auto bytes = [&](int i) { return ((a->rows - 1) * rows[i].row + a->cols) * size_of(rows[i].dtype); };
+  for (const int out : {3, 4})
+    for (const int in : {0, 1, 3}) {
+      if (in >= out || !rows[out].p || !rows[in].p || !overlap(rows[out].p, bytes(out), rows[in].p, bytes(in))) continue;
+      // rows of one stride side by side (columns of one buffer)
+      const int64_t step = rows[out].row * size_of(rows[out].dtype), ow = a->cols * size_of(rows[out].dtype),
+                    iw = a->cols * size_of(rows[in].dtype);
+      if (step == rows[in].row * size_of(rows[in].dtype)) {
+        const int64_t d = reinterpret_cast<intptr_t>(rows[out].p) - reinterpret_cast<intptr_t>(rows[in].p);
+        const int64_t m = (d % step + step) % step;  // out's row begins m bytes behind a row of in
+        if (m >= iw && step - m >= ow) continue;
+      }
+      if (in < 3 && rows[out].p == rows[in].p && rows[out].row == rows[in].row &&
+          size_of(rows[out].dtype) == size_of(rows[in].dtype))
+        continue;  // in place
+      return fail(QMV_ERR_SHAPE, "an output overlaps an input or the other output");
+    }
+  return QMV_OK;
+}
+
 // A paired launch of two matrices of one format, layout and shape (`a` with
 // twice its rows; launch.h): both outputs, or with glu the SwiGLU input.
 static hipError_t pair_launch(int32_t fmt, const GemvCall& a, const void* b_w, float* b_y, int32_t x_dtype,
@@ -210,6 +331,7 @@ static hipError_t pair_launch(int32_t fmt, const GemvCall& a, const void* b_w, f
     case QMV_Q4_K: return gemv_q4_k_pair(a, b_w, b_y, x_dtype, batch, planes, glu, s);
     case QMV_Q5_K: return gemv_q5_k_pair(a, b_w, b_y, x_dtype, batch, planes, glu, s);
     case QMV_Q6_K: return gemv_q6_k_pair(a, b_w, b_y, x_dtype, batch, planes, glu, s);
+    case QMV_MXFP4: return gemv_mxfp4_pair(a, b_w, b_y, x_dtype, batch, glu, s);
     default: return gemv_int4_g128_pair(a, b_w, b_y, x_dtype, batch, glu, s);
   }
 }
@@ -247,6 +369,7 @@ int32_t qmv_block_size(int32_t fmt) {
     case QMV_Q6_K: return 256;
     case QMV_Q5_K: return 256;
     case QMV_INT4_G128: return 128;
+    case QMV_MXFP4: return 32;
     default: return 0;
   }
 }
@@ -261,6 +384,7 @@ uint64_t qmv_packed_size(int32_t fmt, int64_t rows, int64_t cols) {
     case QMV_Q4_K: return nblk * 144;
     case QMV_Q6_K: return nblk * 210;
     case QMV_Q5_K: return nblk * 176;
+    case QMV_MXFP4: return nblk * 17;
     default: return static_cast<uint64_t>(rows) * cols / 2 + nblk * 2;
   }
 }
@@ -353,7 +477,7 @@ int32_t qmv_create_weights(int32_t fmt, int64_t rows, int64_t cols, const void* 
   w.cols = cols;
   w.data = dev_packed;
   w.nbytes = nbytes;
-  w.scales_offset = fmt == QMV_INT4_G128 ? static_cast<uint64_t>(rows * cols / 2) : 0;
+  w.scales_offset = qmv::codes_plane(fmt) ? static_cast<uint64_t>(rows * cols / 2) : 0;
   *out = w;
   return qmv::ok();
 }
@@ -512,6 +636,7 @@ static int32_t gemv_multi_impl(int32_t fmt, int32_t x_dtype, int64_t batch, cons
         case QMV_Q6_K: return qmv::gemv_q6_k_rows(c, k, x_dtype, batch, planes, s);
         case QMV_Q5_K: return qmv::gemv_q5_k_rows(c, k, x_dtype, batch, planes, s);
         case QMV_Q8_0: return qmv::gemv_q8_0_rows(c, k, x_dtype, batch, s);
+        case QMV_MXFP4: return qmv::gemv_mxfp4_rows(c, k, x_dtype, batch, s);
         default: return qmv::gemv_int4_g128_rows(c, k, x_dtype, batch, s);
       }
     };
@@ -542,6 +667,7 @@ static int32_t gemv_multi_impl(int32_t fmt, int32_t x_dtype, int64_t batch, cons
                        : qmv::gemv_q5_k(wide, nw, x_dtype, batch, s);
             break;
           case QMV_Q8_0: e = qmv::gemv_q8_0(wide, nw, x_dtype, batch, s); break;
+          case QMV_MXFP4: e = qmv::gemv_mxfp4(wide, nw, x_dtype, batch, s); break;
           default: e = qmv::gemv_int4_g128(wide, nw, x_dtype, batch, s); break;
         }
       }
@@ -583,6 +709,7 @@ static int32_t gemv_multi_impl(int32_t fmt, int32_t x_dtype, int64_t batch, cons
       e = planes ? qmv::gemv_q6_k_planes(calls, n, x_dtype, batch, s)
                  : qmv::gemv_q6_k(calls, n, x_dtype, batch, s);
       break;
+    case QMV_MXFP4: e = qmv::gemv_mxfp4(calls, n, x_dtype, batch, s); break;
     default: e = qmv::gemv_int4_g128(calls, n, x_dtype, batch, s); break;
   }
   return qmv::from_hip(e, "qmv_gemv launch");
@@ -686,6 +813,27 @@ int32_t qmv_verify(const qmv_verify_args* a, void* workspace, uint64_t workspace
   st = qmv::check_workspace(workspace, workspace_bytes, qmv::verify_workspace(*a), "qmv_verify_workspace_size");
   if (st != QMV_OK) return st;
   return qmv::from_hip(qmv::verify(*a, workspace, static_cast<hipStream_t>(stream)), "qmv_verify launch");
+}
+
+int32_t qmv_quantize(const qmv_weights* W, const void* x, int32_t x_dtype, int64_t x_row, void* stream) {
+  const int32_t st = qmv::check_quantize(W, x, x_dtype, x_row);
+  if (st != QMV_OK) return st;
+  return qmv::from_hip(qmv::mx4_quantize(*W, x, x_dtype, x_row, static_cast<hipStream_t>(stream)),
+                       "qmv_quantize launch");
+}
+
+int32_t qmv_mx4_gemm(const qmv_mx4_args* a, void* stream) {
+  const int32_t st = qmv::check_mx4(a);
+  if (st != QMV_OK) return st;
+  if (a->rows == 0) return qmv::ok();
+  return qmv::from_hip(qmv::mx4_gemm(*a, static_cast<hipStream_t>(stream)), "qmv_mx4_gemm launch");
+}
+
+int32_t qmv_norm(const qmv_norm_args* a, void* stream) {
+  const int32_t st = qmv::check_norm(a);
+  if (st != QMV_OK) return st;
+  if (a->rows == 0) return qmv::ok();
+  return qmv::from_hip(qmv::norm(*a, static_cast<hipStream_t>(stream)), "qmv_norm launch");
 }
 
 int64_t qmv_probe_read_outputs(uint64_t nbytes) { return qmv::probe_read_blocks(nbytes); }

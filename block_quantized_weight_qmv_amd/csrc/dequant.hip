@@ -14,6 +14,7 @@
 // which round once at the subtraction.  fp16 / bf16 outputs are that fp32 value rounded to nearest even.
 #include "device_util.h"
 #include "launch.h"
+#include "mx4.h"
 #include "planes.h"
 
 namespace qmv {
@@ -261,6 +262,7 @@ static hipError_t dequant_fmt(const qmv_weights& W, void* out, int out_dtype, hi
 }
 
 hipError_t dequant(const qmv_weights& W, void* out, int out_dtype, hipStream_t s) {
+  if (W.fmt == QMV_MXFP4) return mx4_dequant(W, out, out_dtype, s);
   if (W.layout == QMV_LAYOUT_PLANES) {
     if (W.fmt == QMV_Q4_K) return dequant_fmt<kQ4KPlanes>(W, out, out_dtype, s);
     if (W.fmt == QMV_Q5_K) return dequant_fmt<kQ5KPlanes>(W, out, out_dtype, s);
@@ -301,6 +303,11 @@ __device__ __forceinline__ void dq_half(const uint8_t* w, uint64_t scales_offset
       const int u = (e < 8 ? q.x : q.y) >> (4 * (e & 7)) & 15;
       v[e] = s * static_cast<float>(u - 8);
     }
+  } else if constexpr (FMT == QMV_MXFP4) {
+    const uint32_t p = ld_u8(w + scales_offset + static_cast<size_t>(r) * (cols / 32) + k / 32);
+    const uint2 q = ld8_any(w + static_cast<size_t>(r) * (cols / 2) + k / 2);
+    mx4_decode8(q.x, p, v);
+    mx4_decode8(q.y, p, v + 8);
   } else {
     const size_t blk = static_cast<size_t>(r) * (cols / 256) + k / 256;
     const int t = k % 256, l = t & 16;
@@ -437,6 +444,7 @@ hipError_t embed(const qmv_weights& W, const int32_t* ids, int64_t n, float scal
     case QMV_Q5_K: return embed_fmt<QMV_Q5_K>(W, ids, n, scale, out, out_dtype, s);
     case QMV_Q6_K: return embed_fmt<QMV_Q6_K>(W, ids, n, scale, out, out_dtype, s);
     case QMV_INT4_G128: return embed_fmt<QMV_INT4_G128>(W, ids, n, scale, out, out_dtype, s);
+    case QMV_MXFP4: return embed_fmt<QMV_MXFP4>(W, ids, n, scale, out, out_dtype, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -67,6 +67,8 @@ hipError_t gemv_q6_k_planes(const GemvCall* calls, int n, int x_dtype, int64_t b
                             hipStream_t s);
 hipError_t gemv_int4_g128(const GemvCall* calls, int n, int x_dtype, int64_t batch,
                           hipStream_t s);
+hipError_t gemv_mxfp4(const GemvCall* calls, int n, int x_dtype, int64_t batch, hipStream_t s);
+hipError_t gemv_mxfp4_rows(const GemvCall* calls, int n, int x_dtype, int64_t batch, hipStream_t s);
 
 // Two matrices of one format, layout and shape on one activation as one
 // launch whose two-row tiles pair row i of each (gemv_pair_kernel): `a`
@@ -85,6 +87,8 @@ hipError_t gemv_q6_k_pair(const GemvCall& a, const void* b_w, float* b_y, int x_
                           bool planes, bool glu, hipStream_t s);
 hipError_t gemv_int4_g128_pair(const GemvCall& a, const void* b_w, float* b_y, int x_dtype, int64_t batch,
                                bool glu, hipStream_t s);
+hipError_t gemv_mxfp4_pair(const GemvCall& a, const void* b_w, float* b_y, int x_dtype, int64_t batch, bool glu,
+                           hipStream_t s);
 
 // Batched Q4_K x bf16 on MFMA (gemm_q4_k_mfma.hip); the GEMV entry points use
 // it for batches of at least kMfmaMinBatch rows.
@@ -171,6 +175,14 @@ size_t attn_workspace(const qmv_attn_args& a);
 hipError_t attn(const qmv_attn_args& a, void* ws, hipStream_t s);
 size_t verify_workspace(const qmv_verify_args& a);
 hipError_t verify(const qmv_verify_args& a, void* ws, hipStream_t s);
+
+// MXFP4 blocks from activations and back (mx4_quant.hip), their products
+// (mx4_gemm.hip) and norms (norm.hip), after validation.
+hipError_t mx4_quantize(const qmv_weights& W, const void* x, int x_dtype, int64_t x_row, hipStream_t s);
+hipError_t mx4_dequant(const qmv_weights& W, void* out, int out_dtype, hipStream_t s);
+bool mx4_gemm_fits(const qmv_mx4_args& a);  // within a launch's workgroups
+hipError_t mx4_gemm(const qmv_mx4_args& a, hipStream_t s);
+hipError_t norm(const qmv_norm_args& a, hipStream_t s);
 
 // Canonical Q4_K / Q5_K / Q6_K blocks -> plane layout (planes.h) at dst.
 hipError_t repack_q4_k_planes(const qmv_weights& src, void* dst, hipStream_t s);

@@ -163,4 +163,15 @@ int32_t qmv_pack_int4_g128(const uint16_t* s_bits, const int8_t* q, int64_t rows
   return qmv::ok();
 }
 
+int32_t qmv_pack_mxfp4(const uint8_t* p, const uint8_t* code, int64_t rows, int64_t cols, uint8_t* out,
+                       uint64_t out_bytes) {
+  const int32_t st = check_common(QMV_MXFP4, p, code, rows, cols, out, out_bytes);
+  if (st != QMV_OK) return st;
+  for (int64_t i = 0; i < rows * cols; ++i)
+    if (code[i] > 15) return qmv::fail(QMV_ERR_RANGE, "mxfp4: code > 15 at %lld", (long long)i);
+  for (int64_t i = 0; i < rows * cols / 2; ++i) out[i] = static_cast<uint8_t>(code[2 * i] | (code[2 * i + 1] << 4));
+  memcpy(out + rows * cols / 2, p, static_cast<size_t>(rows * (cols / 32)));
+  return qmv::ok();
+}
+
 }  // extern "C"

@@ -20,7 +20,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 # the CPU test suite); by default the in-tree libqmv.so.
 LIB_PATH = os.environ.get("QMV_LIBRARY") or os.path.join(PKG_DIR, "libqmv.so")
 
-FMT = {"q8_0": 1, "q4_k": 2, "q6_k": 3, "int4_g128": 4, "q5_k": 5}
+FMT = {"q8_0": 1, "q4_k": 2, "q6_k": 3, "int4_g128": 4, "q5_k": 5, "mxfp4": 8}
 DTYPE = {"f32": 0, "f16": 1, "bf16": 2}
 LAYOUT = {"blocks": 0, "planes": 1}
 
@@ -69,6 +69,24 @@ class QmvVerifyArgs(ctypes.Structure):
                                                "u_accept", "u_sample", "out_tokens", "accepted")]
 
 
+class QmvMx4Args(ctypes.Structure):
+    """Mirror of struct qmv_mx4_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("y_dtype", "epilogue", "experts", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("rows", "y_row")] + \
+               [("W", ctypes.POINTER(QmvWeights)), ("X", ctypes.POINTER(QmvWeights))] + \
+               [(n, ctypes.c_void_p) for n in ("expert_start", "x_index", "y")]
+
+
+class QmvNormArgs(ctypes.Structure):
+    """Mirror of struct qmv_norm_args."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "weight_dtype", "y_dtype", "pre", "post")] + \
+               [("eps", ctypes.c_float), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)] + \
+               [(n, ctypes.c_int64) for n in ("rows", "cols", "residual_row", "block_row", "sum_row", "y_row",
+                                              "gate_row")] + \
+               [(n, ctypes.c_void_p) for n in ("residual", "block", "gate", "pre_weight", "pre_bias", "post_weight",
+                                               "post_bias", "sum", "y")]
+
+
 _lib = None
 
 _i32, _i64, _u64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
@@ -80,6 +98,7 @@ _SIGS = {
     "qmv_pack_q5_k": (_i32, [_p, _p, _p, _p, _p, _i64, _i64, _p, _u64]),
     "qmv_pack_q6_k": (_i32, [_p, _p, _p, _i64, _i64, _p, _u64]),
     "qmv_pack_int4_g128": (_i32, [_p, _p, _i64, _i64, _p, _u64]),
+    "qmv_pack_mxfp4": (_i32, [_p, _p, _i64, _i64, _p, _u64]),
     "qmv_create_weights": (_i32, [_i32, _i64, _i64, _p, _u64, ctypes.POINTER(QmvWeights)]),
     "qmv_planes_size": (_u64, [_i32, _i64, _i64]),
     "qmv_create_weights_planes": (_i32, [_i32, _i64, _i64, _p, _u64, ctypes.POINTER(QmvWeights)]),
@@ -98,6 +117,9 @@ _SIGS = {
     "qmv_attn": (_i32, [ctypes.POINTER(QmvAttnArgs), _p, _u64, _p]),
     "qmv_verify_workspace_size": (_i32, [ctypes.POINTER(QmvVerifyArgs), ctypes.POINTER(_u64)]),
     "qmv_verify": (_i32, [ctypes.POINTER(QmvVerifyArgs), _p, _u64, _p]),
+    "qmv_quantize": (_i32, [ctypes.POINTER(QmvWeights), _p, _i32, _i64, _p]),
+    "qmv_mx4_gemm": (_i32, [ctypes.POINTER(QmvMx4Args), _p]),
+    "qmv_norm": (_i32, [ctypes.POINTER(QmvNormArgs), _p]),
     "qmv_probe_read_outputs": (_i64, [_u64]),
     "qmv_probe_read": (_i32, [_p, _u64, _p, _p]),
     "qmv_probe_copy": (_i32, [_p, _p, _u64, _p]),
@@ -279,6 +301,12 @@ def qmv_pack_int4_g128(s_bits, q, rows: int, cols: int) -> np.ndarray:
     return out
 
 
+def qmv_pack_mxfp4(p, code, rows: int, cols: int) -> np.ndarray:
+    pp, c, out = _c(p, np.uint8), _c(code, np.uint8), _pack_out("mxfp4", rows, cols)
+    _check(lib().qmv_pack_mxfp4(_ptr(pp), _ptr(c), rows, cols, _ptr(out), out.size))
+    return out
+
+
 def pack_fields(fmt: str, fields: dict, rows: int, cols: int) -> np.ndarray:
     """Call the packer of `fmt` with the field arrays named as in synth/."""
     if fmt == "q8_0":
@@ -293,6 +321,8 @@ def pack_fields(fmt: str, fields: dict, rows: int, cols: int) -> np.ndarray:
         return qmv_pack_q6_k(fields["d_bits"], fields["sc"], fields["q"], rows, cols)
     if fmt == "int4_g128":
         return qmv_pack_int4_g128(fields["s_bits"], fields["q"], rows, cols)
+    if fmt == "mxfp4":
+        return qmv_pack_mxfp4(fields["p"], fields["code"], rows, cols)
     raise ValueError(fmt)
 
 
@@ -625,6 +655,124 @@ def qmv_verify(a: QmvVerifyArgs, workspace, workspace_bytes: int, stream=None) -
         _check_dev(workspace, "workspace", None, workspace_bytes)
         _check_with("workspace", workspace, "logits", logits)
     _check(lib().qmv_verify(ctypes.byref(a), _ptr(workspace), workspace_bytes, _stream(stream, logits, workspace)))
+
+
+def qmv_quantize(W: QmvWeights, x, stream=None) -> None:
+    """W = x in W's format (mxfp4), written to the bytes that W describes.  x: a device tensor [W.rows, W.cols] of float32,
+    float16 or bfloat16, its rows of any stride."""
+    name = str(getattr(x, "dtype", "")).replace("torch.", "")
+    if name not in ("float32", "float16", "bfloat16"):
+        raise QmvError(-6, f"x: {name or type(x)}, expected a float32, float16 or bfloat16 tensor")
+    _check_view(x, "x", name, 2)
+    if tuple(x.shape) != (W.rows, W.cols):
+        raise QmvError(-3, f"x: shape {tuple(x.shape)}, expected {(W.rows, W.cols)}")
+    _check_with("W", getattr(W, "owner", None), "x", x)
+    _check(lib().qmv_quantize(ctypes.byref(W), x.data_ptr(), _dtype(x.dtype), x.stride(0) if W.rows > 1 else W.cols,
+                              _stream(stream, x)))
+
+
+def qmv_create_mx4(W: QmvWeights, X: QmvWeights, y, *, swiglu: bool = False, expert_start=None,
+                   x_index=None) -> QmvMx4Args:
+    """Checked arguments of qmv_mx4_gemm, kept alive with them.
+
+    W, X: mxfp4 descriptors, the weights (with expert_start the experts' matrices one after another) and the
+    activations; y: a device tensor [rows, outputs] of float32, float16 or bfloat16, its rows of any stride;
+    expert_start [experts + 1] and x_index [rows] int32."""
+    a = QmvMx4Args()
+    name = str(getattr(y, "dtype", "")).replace("torch.", "")
+    if name not in ("float32", "float16", "bfloat16"):
+        raise QmvError(-6, f"y: {name or type(y)}, expected a float32, float16 or bfloat16 tensor")
+    _check_view(y, "y", name, 2)
+    rows, n = (int(v) for v in y.shape)
+    if expert_start is not None:
+        _check_vec(expert_start, "expert_start", _I32, 2)
+        a.experts = int(expert_start.numel()) - 1
+    if x_index is not None:
+        _check_vec(x_index, "x_index", _I32, rows)
+    parts = max(1, a.experts) * (2 if swiglu else 1)
+    if W.rows != n * parts:
+        raise QmvError(-3, f"W: {W.rows} rows, y's {n} columns need {n * parts}")
+    a.y_dtype, a.epilogue, a.rows = _dtype(y.dtype), int(bool(swiglu)), rows
+    a.y_row = y.stride(0) if rows > 1 else n
+    a.W, a.X = ctypes.pointer(W), ctypes.pointer(X)
+    named = dict(y=y, W=getattr(W, "owner", None), X=getattr(X, "owner", None), expert_start=expert_start,
+                 x_index=x_index)
+    _check_one_device(list(named.items()))
+    a.expert_start, a.x_index, a.y = _ptr(expert_start), _ptr(x_index), _ptr(y)
+    a.owner = dict(named, W=W, X=X)
+    return a
+
+
+def qmv_mx4_gemm(a: QmvMx4Args, stream=None) -> None:
+    """y = X W^T of MXFP4 activations and weights, dense or by expert (qmv_create_mx4)."""
+    owner = getattr(a, "owner", None)
+    _check(lib().qmv_mx4_gemm(ctypes.byref(a), _stream(stream, owner["y"] if owner else None)))
+
+
+NORM = {None: 0, "rms": 1, "layer": 2}
+
+
+def qmv_create_norm(residual, y=None, *, pre=None, pre_weight=None, pre_bias=None, block=None, post=None,
+                    post_weight=None, post_bias=None, gate=None, scale: float = 1.0, sum_out=None,
+                    eps: float = 1e-6) -> QmvNormArgs:
+    """Checked arguments of qmv_norm, kept alive with them.
+
+    residual, block, sum_out [rows, cols] and gate [cols] or [rows, cols] of one type (float32, float16 or bfloat16), y
+    [rows, cols] of any of them, rows of any stride; weights and biases [cols], of one type; pre, post: None, "rms" or
+    "layer"."""
+    a = QmvNormArgs()
+    floats = ("float32", "float16", "bfloat16")
+    name = str(getattr(residual, "dtype", "")).replace("torch.", "")
+    if name not in floats:
+        raise QmvError(-6, f"residual: {name or type(residual)}, expected a float32, float16 or bfloat16 tensor")
+    _check_view(residual, "residual", name, 2)
+    rows, cols = (int(v) for v in residual.shape)
+    a.dtype = a.y_dtype = a.weight_dtype = _dtype(residual.dtype)
+    for what, t in (("block", block), ("sum_out", sum_out), ("y", y)):
+        if t is None:
+            continue
+        kind = str(getattr(t, "dtype", "")).replace("torch.", "")
+        if what == "y" and kind not in floats:
+            raise QmvError(-6, f"y: {kind or type(t)}, expected a float32, float16 or bfloat16 tensor")
+        _check_view(t, what, kind if what == "y" else name, 2)
+        if tuple(t.shape) != (rows, cols):
+            raise QmvError(-3, f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if y is not None:
+        a.y_dtype = _dtype(y.dtype)
+    weights = dict(pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight, post_bias=post_bias)
+    kinds = {str(getattr(t, "dtype", type(t))).replace("torch.", "") for t in weights.values() if t is not None}
+    if len(kinds) > 1 or not kinds <= set(floats):
+        raise QmvError(-6, f"weights and biases: {sorted(kinds)}, expected one of {floats}")
+    for what, t in weights.items():
+        if t is not None:
+            _check_vec(t, what, tuple(kinds), cols)
+            a.weight_dtype = _dtype(t.dtype)
+    if gate is not None:
+        _check_view(gate, "gate", name, gate.dim() if getattr(gate, "dim", None) and gate.dim() in (1, 2) else 2)
+        if tuple(gate.shape) not in ((cols,), (rows, cols)):
+            raise QmvError(-3, f"gate: shape {tuple(gate.shape)}, expected {(cols,)} or {(rows, cols)}")
+    for kind in (pre, post):
+        if kind not in NORM:
+            raise QmvError(-6, f"norm {kind!r}, expected one of {tuple(NORM)}")
+    a.pre, a.post, a.rows, a.cols, a.eps, a.scale = NORM[pre], NORM[post], rows, cols, eps, scale
+
+    def stride(t):
+        return cols if t is None or rows <= 1 else t.stride(0)
+
+    a.residual_row, a.block_row, a.sum_row, a.y_row = stride(residual), stride(block), stride(sum_out), stride(y)
+    a.gate_row = gate.stride(0) if gate is not None and gate.dim() == 2 and rows > 1 else 0
+    named = dict(residual=residual, block=block, gate=gate, sum_out=sum_out, y=y, **weights)
+    _check_one_device(list(named.items()))
+    for field, t in named.items():
+        setattr(a, "sum" if field == "sum_out" else field, _ptr(t))
+    a.owner = named
+    return a
+
+
+def qmv_norm(a: QmvNormArgs, stream=None) -> None:
+    """The norms around a block and the residual between them (qmv_create_norm)."""
+    owner = getattr(a, "owner", None)
+    _check(lib().qmv_norm(ctypes.byref(a), _stream(stream, owner["residual"] if owner else None)))
 
 
 def qmv_probe_read_outputs(nbytes: int) -> int:

@@ -42,6 +42,13 @@
  *         holding u_{2j} (bits 0-3) and u_{2j+1} (bits 4-7), u = q+8; then a
  *         scales plane of rows*(cols/128) fp16 at scales_offset = rows*cols/2.
  *         w_k = s_{k/128}*(u_k-8).
+ *     MXFP4 (QK 32): codes plane rows*cols/2 bytes, byte j of a row holding
+ *         code 2j (bits 0-3) and code 2j+1 (bits 4-7), a code being a 4-bit
+ *         float (bit 3 the sign, bits 0-2: 0, .5, 1, 1.5, 2, 3, 4, 6); then a
+ *         scales plane of rows*(cols/32) bytes p at scales_offset =
+ *         rows*cols/2.  w_k = 2^(p_{k/32} - 127) * code_k; p = 255 makes the
+ *         block NaN.  (OCP microscaling's MXFP4; the planes are this
+ *         library's order.)
  *   GEMV: y[b][r] = sum_k W[r][k] * x[b][k], x [batch][cols] row-major,
  *   y [batch][rows] fp32 row-major, overwritten.  Products and sums are
  *   carried in fp32; activations are converted exactly to fp32 (f16 and
@@ -74,7 +81,8 @@ enum {
   QMV_Q4_K = 2,
   QMV_Q6_K = 3,
   QMV_INT4_G128 = 4,
-  QMV_Q5_K = 5
+  QMV_Q5_K = 5,
+  QMV_MXFP4 = 8
 };
 
 enum { QMV_F32 = 0, QMV_F16 = 1, QMV_BF16 = 2 };
@@ -123,19 +131,20 @@ enum {
  * caller-owned; it only points at the packed bytes, which must stay alive
  * (and unmodified) until every enqueued call that reads them has finished. */
 typedef struct qmv_weights {
-  int32_t fmt;            /* QMV_Q8_0 .. QMV_Q5_K                            */
+  int32_t fmt;            /* QMV_Q8_0 .. QMV_MXFP4                           */
   int32_t layout;         /* QMV_LAYOUT_BLOCKS (0) or QMV_LAYOUT_PLANES      */
   int64_t rows, cols;     /* logical shape of W                              */
   const void* data;       /* device pointer to the packed bytes (16 B aligned)*/
   uint64_t nbytes;        /* == qmv_packed_size(fmt, rows, cols), or         */
                           /* qmv_planes_size for QMV_LAYOUT_PLANES           */
-  uint64_t scales_offset; /* INT4_G128: byte offset of the scales plane;     */
+  uint64_t scales_offset; /* INT4_G128, MXFP4: byte offset of the scales     */
+                          /* plane;                                          */
                           /* QMV_LAYOUT_PLANES: offset a of code plane A;    */
                           /* 0 for the block formats                         */
 } qmv_weights;
 
-/* Codes per block: 32, 256, 256, 128, 256 (Q8_0, Q4_K, Q6_K, INT4_G128,
- * Q5_K); 0 for an unknown format. */
+/* Codes per block: 32, 256, 256, 128, 256, 32 (Q8_0, Q4_K, Q6_K, INT4_G128,
+ * Q5_K, MXFP4); 0 for an unknown format. */
 int32_t qmv_block_size(int32_t fmt);
 
 /* Bytes of a packed rows x cols tensor; 0 if fmt is unknown, rows or cols < 1
@@ -177,8 +186,12 @@ int32_t qmv_pack_int4_g128(const uint16_t* s_bits, const int8_t* q,
                            int64_t rows, int64_t cols, uint8_t* out,
                            uint64_t out_bytes);
 
+/* MXFP4: p [rows][cols/32] (any byte); code [rows][cols] in 0..15. */
+int32_t qmv_pack_mxfp4(const uint8_t* p, const uint8_t* code, int64_t rows,
+                       int64_t cols, uint8_t* out, uint64_t out_bytes);
+
 /* Bytes of the QMV_LAYOUT_PLANES layout of a rows x cols tensor; 0 if the
- * format has no plane layout (Q8_0, INT4_G128) or the shape is
+ * format has no plane layout (Q8_0, INT4_G128, MXFP4) or the shape is
  * invalid. */
 uint64_t qmv_planes_size(int32_t fmt, int64_t rows, int64_t cols);
 
@@ -521,6 +534,114 @@ typedef struct qmv_verify_args {
 int32_t qmv_verify_workspace_size(const qmv_verify_args* a, uint64_t* bytes);
 int32_t qmv_verify(const qmv_verify_args* a, void* workspace,
                    uint64_t workspace_bytes, void* stream);
+
+/* ---- A feed-forward block in MXFP4, dense or of experts -----------------
+ * qmv_norm joins the block before to the residual and norms the sum, and
+ * qmv_quantize brings it to MXFP4; qmv_mx4_gemm multiplies it with the gate and
+ * up weights, and, quantized again, with the down weights.  (MXFP4 weights are
+ * also a format of qmv_gemv and its kin, whose activations stay exact.)
+ * Inference only: quantized weights are frozen, and none of these calls has a
+ * gradient. */
+
+/* W = x in W's format, on the device: the inverse of qmv_dequant.  W describes
+ * the bytes that are written (writable device memory of nbytes bytes; its
+ * layout QMV_LAYOUT_BLOCKS); fmt QMV_MXFP4 only (QMV_ERR_UNSUPPORTED otherwise).
+ * x is [W->rows][W->cols] of x_dtype, x_row elements from one row to the next
+ * (at least cols, a multiple of 8), 16-byte aligned, not overlapping W's bytes
+ * (QMV_ERR_SHAPE).  For each 32 columns, with top = max |x|:
+ *   p = max(0, floor(log2 top) - 2 + 127), code = x / 2^(p-127) rounded to the
+ *   nearest code, ties to the even one, above 6 to 6, the sign kept on zeros.
+ * (The conversion of OCP microscaling: top lands in [4, 8).)  A block without a
+ * nonzero number has p = 0; one with a NaN or an infinity has p = 255 and zero
+ * codes, and reads back as NaN.  Enqueues only; no workspace; legal inside HIP
+ * stream capture. */
+int32_t qmv_quantize(const qmv_weights* W, const void* x, int32_t x_dtype,
+                     int64_t x_row, void* stream);
+
+enum { QMV_MX4_PLAIN = 0, QMV_MX4_SWIGLU = 1 };
+
+/* Arguments of qmv_mx4_gemm. */
+typedef struct qmv_mx4_args {
+  int32_t y_dtype;        /* QMV_F32, QMV_F16 or QMV_BF16                    */
+  int32_t epilogue;       /* QMV_MX4_PLAIN or QMV_MX4_SWIGLU                 */
+  int32_t experts;        /* 0: one matrix; else the matrices of W, 1..2^16  */
+  int32_t reserved;       /* 0                                               */
+  int64_t rows;           /* rows of y                                       */
+  int64_t y_row;          /* elements from one row of y to the next          */
+  const qmv_weights* W;   /* MXFP4; the experts' matrices one after another, */
+                          /* so W->rows is a multiple of experts             */
+  const qmv_weights* X;   /* MXFP4, the activations, W->cols columns         */
+  const int32_t* expert_start; /* [experts + 1] with experts, else NULL      */
+  const int32_t* x_index;      /* NULL, or [rows]                            */
+  void* y;                /* aligned by its type                             */
+} qmv_mx4_args;
+
+/* y[i] = W_e X[x_index[i]] (X[i] without x_index), with e the expert whose rows
+ * hold i: expert_start[e] <= i < expert_start[e + 1], nondecreasing numbers in
+ * device memory; without experts, W for every row.  Rows of y before the first
+ * and behind the last expert's are left as they were.  With m = W->rows /
+ * max(experts, 1) outputs of a matrix:
+ *   QMV_MX4_PLAIN:  y is [rows][m];
+ *   QMV_MX4_SWIGLU: y is [rows][m/2], silu(g) u with g the first half of the
+ *     matrix's outputs (the gate's rows) and u the second (up), silu(g) =
+ *     g / (1 + e^-g), within a few ulp of fp32 before the rounding to y's type.
+ * Products of codes are exact, sums fp32, in an order that depends on the
+ * sizes alone: results do not depend on timing.  One to a few rows of a matrix
+ * read it once; many run as tiles on the matrix cores.
+ * Device integers are clamped: an x_index outside [0, X->rows) makes a row of
+ * zeros, expert_start counts as its running maximum, cut to [0, rows].
+ * A NaN block of W makes its output NaN in every row, one of X its row.
+ * y must not overlap what the call reads.  rows = 0 launches nothing.
+ * Errors: QMV_ERR_NULL, QMV_ERR_FORMAT (W or X not MXFP4, or any error of a
+ * descriptor), QMV_ERR_SHAPE (columns differ, W->rows no multiple of experts or
+ * of its halves, more rows than X without x_index, y_row below y's columns, y
+ * overlaps W or X), QMV_ERR_ALIGN, QMV_ERR_UNSUPPORTED (dtype, epilogue, sizes
+ * past the limits: 2^22 rows, 2^26 outputs of a matrix).  Enqueues only; no workspace; legal inside
+ * HIP stream capture. */
+int32_t qmv_mx4_gemm(const qmv_mx4_args* a, void* stream);
+
+enum { QMV_NORM_NONE = 0, QMV_NORM_RMS = 1, QMV_NORM_LAYER = 2 };
+
+/* Arguments of qmv_norm.  Row strides count elements; pointers are aligned by
+ * their type (16-byte aligned rows of a multiple of 8 columns run fastest). */
+typedef struct qmv_norm_args {
+  int32_t dtype;          /* residual, block, gate and sum                   */
+  int32_t weight_dtype;   /* the weights and biases                          */
+  int32_t y_dtype;
+  int32_t pre, post;      /* QMV_NORM_NONE, QMV_NORM_RMS or QMV_NORM_LAYER   */
+  float eps;              /* added to the mean square; >= 0 and finite       */
+  float scale;            /* of the block's output; finite                   */
+  int32_t reserved;       /* 0                                               */
+  int64_t rows, cols;     /* cols 1..32768                                   */
+  int64_t residual_row, block_row, sum_row, y_row;
+  int64_t gate_row;       /* 0: one gate for all rows                        */
+  const void* residual;   /* [rows][cols]                                    */
+  const void* block;      /* NULL, or [rows][cols]                           */
+  const void* gate;       /* NULL, or [cols] or [rows][cols]; with block     */
+  const void* pre_weight;  /* each NULL (1, 0) or [cols]; with their norm    */
+  const void* pre_bias;
+  const void* post_weight;
+  const void* post_bias;
+  void* sum;              /* NULL, or [rows][cols]                           */
+  void* y;                /* NULL, or [rows][cols]                           */
+} qmv_norm_args;
+
+/* The norms before and after a block, with the residual between them:
+ *   s = residual + scale * gate . post(block)   (s = residual without block)
+ *   sum = s,  y = pre(s)
+ * norm(x) = (x - c) / sqrt(mean((x - c)^2) + eps) * weight + bias, c = 0 for
+ * QMV_NORM_RMS and the row's mean for QMV_NORM_LAYER; QMV_NORM_NONE is x.  All
+ * of it in fp32, each output rounded once; y is that of the unrounded s.
+ * sum or y may be residual or block themselves (same address, stride and
+ * element size); any other overlap of an output with them or with the other
+ * output is refused (QMV_ERR_SHAPE), and outputs must not overlap the gate,
+ * weights and biases.  rows = 0 launches nothing.
+ * Errors: QMV_ERR_NULL (residual, or neither sum nor y), QMV_ERR_SHAPE (counts,
+ * a stride below cols, gate or post without block, weights or biases without
+ * their norm, pre without y), QMV_ERR_ALIGN, QMV_ERR_RANGE (eps, scale),
+ * QMV_ERR_UNSUPPORTED (dtypes, kinds, sizes past the limits).  Enqueues only;
+ * no workspace; legal inside HIP stream capture. */
+int32_t qmv_norm(const qmv_norm_args* a, void* stream);
 
 /* Measurement kernels for the HBM roofline (not part of the GEMV path).
  * qmv_probe_read streams nbytes (multiple of 16) from src with nontemporal
