@@ -38,48 +38,105 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.f + e) * u;
 }
 
-// Tile t of BM rows over the experts' groups: its expert, first row and the
-// group's end.  Groups come from expert_start as its running maximum, clamped
-// to the rows there are, so that no content reaches outside them.  All lanes of
-// a wave call it together.  False: there are fewer tiles.
-__device__ __forceinline__ bool find_tile(const Mx4Launch& a, int bm, int t, int& e, int& row, int& end) {
-  if (!a.expert_start) {
-    e = 0, row = t * bm, end = a.rows;
-    return row < end;
-  }
-  const int lane = __lane_id();
-  int carry = min(max(a.expert_start[0], 0), a.rows);
-  for (int base = 0; base < a.experts; base += 64) {
-    const int i = base + lane;
-    int last = i < a.experts ? min(max(a.expert_start[i + 1], 0), a.rows) : 0;
+// The experts' groups of rows come from expert_start as its running maximum,
+// clamped to the rows there are, so that no content reaches outside them.  All
+// lanes of a wave call together; lane l holds expert base + l: its first row,
+// its end, and the tiles of bm rows up to and with its own.
+struct Groups {
+  int first, last, sum;
+  __device__ __forceinline__ void load(const Mx4Launch& a, int bm, int base, int carry, int before) {
+    const int lane = __lane_id(), i = base + lane;
+    last = i < a.experts ? min(max(a.expert_start[i + 1], 0), a.rows) : 0;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(last, d);
       last = lane >= d ? max(last, o) : last;
     }
     last = max(last, carry);
-    int first = __shfl_up(last, 1);
+    first = __shfl_up(last, 1);
     first = lane ? first : carry;
-    const int mine = (last - first + bm - 1) / bm;
-    int sum = mine;
+    sum = (last - first + bm - 1) / bm;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(sum, d);
       sum = lane >= d ? sum + o : sum;
     }
-    const uint64_t past = __ballot(t < sum);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      e = base + l;
-      row = __shfl(first, l) + (t - __shfl(sum - mine, l)) * bm;
-      end = __shfl(last, l);
-      return true;
-    }
-    t -= __shfl(sum, 63);
-    carry = __shfl(last, 63);
+    sum += before;
   }
-  return false;
+};
+
+// The lane's number, or what follows from it, worked out here again: numbers that
+// stay the same from tile to tile would otherwise be kept in registers, which
+// the products need.
+__device__ __forceinline__ int again(int v) {
+  __asm__ __volatile__("" : "+v"(v));
+  return v;
 }
+
+// A tile: its expert, first row and end of the group, and its column of tiles.
+struct Tile {
+  int e, row, end, tn;
+};
+
+// The tiles of a launch in the order they are worked on.  Workgroups go to the
+// eight XCDs in turn, each with an L2 of its own: an XCD takes a run of
+// consecutive tiles, in bands of kBand tiles of rows, so that the 32 tiles it
+// works on together share eight row tiles and four column tiles.
+constexpr int kBand = 8;
+struct Tiles {
+  Groups g;
+  int tiles_m, tiles_n, bm, carry;
+
+  __device__ __forceinline__ void init(const Mx4Launch& a, int bm_, int tiles_n_) {
+    bm = bm_, tiles_n = tiles_n_;
+    if (!a.expert_start) {
+      tiles_m = (a.rows + bm - 1) / bm;
+      return;
+    }
+    carry = min(max(a.expert_start[0], 0), a.rows);
+    int c = carry;
+    tiles_m = 0;
+    for (int base = 0; base < a.experts; base += 64) {
+      g.load(a, bm, base, c, tiles_m);
+      c = __builtin_amdgcn_readlane(g.last, 63), tiles_m = __builtin_amdgcn_readlane(g.sum, 63);
+    }
+  }
+
+  // This XCD's run: first tile and end.
+  __device__ __forceinline__ void run(int& first, int& end) const {
+    const int total = tiles_m * tiles_n, xcd = blockIdx.x & 7, each = total >> 3;
+    first = xcd * each + min(xcd, total & 7);
+    end = first + each + (xcd < (total & 7));
+  }
+
+  __device__ __forceinline__ Tile at(const Mx4Launch& a, int i) {
+    const int band = i / (kBand * tiles_n), in = i - band * (kBand * tiles_n), wide = min(kBand, tiles_m - band * kBand);
+    Tile t;
+    t.tn = in / wide;
+    const int m = band * kBand + in - t.tn * wide;
+    if (!a.expert_start) {
+      t.e = 0, t.row = m * bm, t.end = a.rows;
+      return t;
+    }
+    t.e = 0;
+    if (a.experts > 64) {  // more than one scan: find its part again
+      int c = carry, before = 0;
+      for (;; t.e += 64) {
+        g.load(a, bm, t.e, c, before);
+        before = __builtin_amdgcn_readlane(g.sum, 63);
+        if (m < before) break;
+        c = __builtin_amdgcn_readlane(g.last, 63);
+      }
+    }
+    const int l = __builtin_ctzll(__ballot(m < g.sum));
+    const int first = __builtin_amdgcn_readlane(g.first, l);
+    t.e += l;
+    t.end = __builtin_amdgcn_readlane(g.last, l);
+    // tiles of this group from m on: those up to its end
+    t.row = first + (m - (__builtin_amdgcn_readlane(g.sum, l) - (t.end - first + bm - 1) / bm)) * bm;
+    return t;
+  }
+};
 
 __device__ __forceinline__ v4f_t mfma4(const uint4& a, const uint4& b, v4f_t c, uint32_t sa, uint32_t sb) {
   const v8i_t va = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
@@ -123,9 +180,14 @@ template <int MT, int OUT, bool GLU>
 __global__ void __launch_bounds__(256)
 mx4_stream_kernel(const Mx4Launch a, int tiles_n) {
   __shared__ float part[4][2 * MT * 4][64];
-  const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
-  int e, row, end;
-  if (!find_tile(a, 16 * MT, tm, e, row, end)) return;
+  Tiles tiles;
+  tiles.init(a, 16 * MT, tiles_n);
+  int first, run_end;
+  tiles.run(first, run_end);
+  first += blockIdx.x >> 3;
+  if (first >= run_end) return;
+  const Tile at = tiles.at(a, first);
+  const int e = at.e, row = at.row, end = at.end, tn = at.tn;
   const int lane = __lane_id(), wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int blocks = a.k / 32;
   const int64_t kc = a.k / 2;
@@ -220,175 +282,315 @@ __device__ __forceinline__ void copy16(const uint8_t* src, uint32_t lds) {
   __asm__ __volatile__("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(lds) : "m0");
 }
 
-// Sixteen-row groups of a tile whose scales share a dword.
-constexpr int kQuad = 4;
+// The first of the four outputs that lane quarter q holds of group p, among
+// its wave's: 16 bytes of a lane, and 64 of four, are neighbours in y.
+template <int OUT>
+__device__ __forceinline__ int place(int p, int q) {
+  return OUT == QMV_F32 ? 16 * p + 4 * q : 32 * (p >> 1) + 8 * q + 4 * (p & 1);
+}
 
-// Many activation rows: a tile of 16 WN TN weight rows x 16 WM TM activation
+// Place of the 16-byte piece `piece` among the four of row r (of 64 bytes in
+// LDS): a read of 16 rows at one piece meets 16 different places of the 256
+// bytes that LDS serves a clock, in the order it takes lanes.
+__device__ __forceinline__ int slot4(int piece, int r) { return piece ^ (0x78 >> (r >> 1 & 6) & 3); }
+
+// Many activation rows: tiles of 16 WN TN weight rows x 16 WM TM activation
 // rows, WN x WM waves of TN x TM matrix instructions each.
+//
+// A stage is 128 columns of all the tile's rows, copied straight to LDS, into a
+// ring of four: while stage s is multiplied, stage s + 1 is read into registers
+// two fragments ahead of its use, and s + 2 and s + 3 are on their way.  One
+// barrier a stage says both that stage s + 1 has come and that stage s - 1 is
+// read.  Scales take another way (a row's are too few bytes, at any alignment,
+// for copies): 64 blocks' bytes of each row are loaded by four lanes, turned so
+// that a lane's four stages are a dword, and kept in LDS; the matrix
+// instruction picks the stage's byte.
+//
+// A workgroup stays for as many tiles as there are (grid = what the GPU holds):
+// the next tile's first stages, and its scales, are loaded while this one's
+// last stages are multiplied, and its results leave while the next one begins.
 template <int WN, int WM, int TN, int TM, int OUT, bool GLU>
-__global__ void __launch_bounds__(64 * WN * WM)
+__global__ void __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, 2)))
 mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
-  constexpr int kWaves = WN * WM, BN = 16 * WN * TN, BM = 16 * WM * TM, kRows = BN + BM;
-  constexpr int kCopies = kRows / 8 / kWaves;  // copy instructions of a wave for a stage: 8 rows x 128 bytes each
-  constexpr int kScaleRows = (kRows + 64 * kWaves - 1) / (64 * kWaves);
-  constexpr int kQuads = kRows / 16 / kQuad;
-  static_assert(kRows % (8 * kWaves) == 0 && TN % kQuad == 0 && TM % kQuad == 0, "whole copies and scale dwords");
-  __shared__ __attribute__((aligned(128))) uint8_t tile[2][kRows * 128];
-  __shared__ uint32_t scales[2][8][kQuads][16];  // [stage][block][four groups][row]: a byte for each group
-  const int total = gridDim.x, tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
-  (void)total;
-  int e, row, end;
-  if (!find_tile(a, BM, tm, e, row, end)) return;
+  constexpr int kWaves = WN * WM, BN = 16 * WN * TN, BM = 16 * WM * TM, kRows = BN + BM, kStage = kRows * 64;
+  constexpr int kCopies = kRows / 16 / kWaves;  // a wave's copy instructions of a stage: 16 rows x 64 bytes each
+  constexpr int kOuts = 16 * TN / (GLU ? 2 : 1);  // outputs of a wave's rows
+  constexpr int kAhead = 2;                       // weight fragments read ahead of their use
+  static_assert(kRows % (16 * kWaves) == 0 && kStage / kWaves == 4096, "whole copies; 4 KB of a stage to a wave");
+  __shared__ __attribute__((aligned(128))) uint8_t ring[4 * kStage];
+  __shared__ __attribute__((aligned(128))) uint8_t scales[kRows * 32];
   const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blocks = a.k / 32, stages = (blocks + 7) / 8;
-  const int64_t kc = a.k / 2;
-
-  // The matrix row of row t of the tile: weights first.  A wave's groups of 16
-  // weight rows are dealt so that a lane's results are neighbours in y.
-  auto source = [&](int t, const uint8_t*& codes, const uint8_t*& powers) {
-    if (t < BN) {
-      const int w = t / (16 * TN), g = t / 16 % TN, q = t / 4 & 3, i = t & 3;
-      int64_t j;
-      if constexpr (GLU) {
-        const int n = tn * (BN / 2) + w * (8 * TN) + q * (2 * TN) + (g >> 1) * 4 + i;
-        j = min(n, a.n - 1) + static_cast<int64_t>(g & 1) * a.n;
-      } else {
-        j = min(tn * BN + w * (16 * TN) + q * (4 * TN) + g * 4 + i, a.n - 1);
-      }
-      j += static_cast<int64_t>(e) * (GLU ? 2 : 1) * a.n;
-      codes = a.w + j * kc;
-      powers = a.ws + j * blocks;
-    } else {
-      const int i = min(row + t - BN, end - 1);
-      int64_t j = a.x_index ? a.x_index[i] : i;
-      if (j < 0 || j >= a.x_rows) j = 0;  // (such a row's outputs are zeros below)
-      codes = a.x + j * kc;
-      powers = a.xs + j * blocks;
-    }
-  };
-
-  // Copies: lane l of copy c takes 16 bytes of row 8 (kCopies wave + c) + l / 8,
-  // the block that the permutation puts into slot l % 8.
-  const uint8_t* src[kCopies];
-  int block[kCopies];
-#pragma unroll
-  for (int c = 0; c < kCopies; ++c) {
-    const int t = 8 * (kCopies * wave + c) + (lane >> 3);
-    const uint8_t* unused;
-    source(t, src[c], unused);
-    block[c] = (lane & 7) ^ ((t >> 1) & 7);
-  }
-  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(&tile[0][0]));
-  const uint8_t* sp[kScaleRows];
-#pragma unroll
-  for (int c = 0; c < kScaleRows; ++c) {
-    const uint8_t* unused;
-    source(min(static_cast<int>(threadIdx.x) + c * 64 * kWaves, kRows - 1), unused, sp[c]);
-  }
-  auto copy_stage = [&](int s) {
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      copy16(src[c] + 16 * min(8 * s + block[c], blocks - 1),
-             lds + (s & 1) * (kRows * 128) + 1024 * (kCopies * wave + c));
-  };
-  uint2 sv[kScaleRows];
-  auto load_scales = [&](int s) {
-#pragma unroll
-    for (int c = 0; c < kScaleRows; ++c) {
-      if (8 * s + 8 <= blocks) {
-        sv[c] = ld8_any(sp[c] + 8 * s);
-      } else {
-        uint32_t d[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i / 4] |= static_cast<uint32_t>(sp[c][min(8 * s + i, blocks - 1)]) << (8 * (i & 3));
-        sv[c] = make_uint2(d[0], d[1]);
-      }
-    }
-  };
-  auto keep_scales = [&](int s) {
-#pragma unroll
-    for (int c = 0; c < kScaleRows; ++c) {
-      const int t = static_cast<int>(threadIdx.x) + c * 64 * kWaves;
-      if (kRows % (64 * kWaves) != 0 && t >= kRows) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint8_t*>(&scales[s & 1][i][t / 16 / kQuad][t & 15])[t / 16 % kQuad] =
-            static_cast<uint8_t>((i < 4 ? sv[c].x : sv[c].y) >> (8 * (i & 3)));
-    }
-  };
-
   const int wn = wave % WN, wm = wave / WN, r = lane & 15, g = lane >> 4;
-  v4f_t acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+  const int blocks = a.k / 32, stages = (blocks + 3) / 4;
+  Tiles tiles;
+  tiles.init(a, BM, tiles_n);
+  int at, run_end;
+  tiles.run(at, run_end);
+  at += blockIdx.x >> 3;
+  const int step = gridDim.x >> 3;
+  if (at >= run_end) return;
+  Tile tile = tiles.at(a, at), next = tile;
 
-  copy_stage(0);
-  load_scales(0);
-  for (int s = 0; s < stages; ++s) {
-    keep_scales(s);
+  // Row t of a tile in the matrices: weights first.  A wave's groups of 16
+  // weight rows are dealt so that a lane's results are neighbours in y.
+  auto weight_row = [&](const Tile& to, int t) {
+    const int w = t / (16 * TN), gr = t / 16 % TN, q = t / 4 & 3, i = t & 3;
+    const int n = to.tn * (WN * kOuts) + w * kOuts + place<OUT>(GLU ? gr >> 1 : gr, q) + i;
+    return static_cast<uint32_t>((to.e * (GLU ? 2 : 1) + (GLU ? gr & 1 : 0)) * a.n + min(n, a.n - 1));
+  };
+  auto activation_row = [&](int i) {  // (past the group's end: its last row again, not stored)
+    const int j = a.x_index ? a.x_index[i] : i;
+    return j >= 0 && j < a.x_rows ? j : -1;
+  };
+
+  // Lane l of copy c serves row 16 (kCopies wave + c) + l / 4, piece l % 4.  A
+  // row is known by its first block's number: 16 bytes of codes, one of scale.
+  const bool weights = wave < BN / 16 / kCopies;  // this wave copies weight rows, or activation rows
+  const uint8_t* codes = weights ? a.w : a.x;
+  const uint8_t* powers = weights ? a.ws : a.xs;
+  uint32_t first[kCopies], next_first[kCopies];
+  uint32_t none = 0, next_none = 0;  // bit j: this lane's activation row 16 j + r has no index
+  auto find_rows = [&](const Tile& to) {
+    const int lane = again(threadIdx.x & 63), r = lane & 15;
+    unrolled<kCopies>([&](auto c) {
+      const int t = 16 * (kCopies * wave + c) + (lane >> 2);
+      next_first[c] = weights ? 0 : max(activation_row(min(to.row + t - BN, to.end - 1)), 0);
+    });
+    next_none = 0;
+    if (a.x_index) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        next_none |= activation_row(min(to.row + 16 * (wm * TM + j) + r, to.end - 1)) < 0 ? 1u << j : 0;
+    }
+  };
+  auto find_blocks = [&](const Tile& to) {
+    const int lane = again(threadIdx.x & 63);
+    unrolled<kCopies>([&](auto c) {
+      const int t = 16 * (kCopies * wave + c) + (lane >> 2);
+      next_first[c] = (weights ? weight_row(to, t) : next_first[c]) * static_cast<uint32_t>(blocks);
+    });
+  };
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(&ring[0]));
+  const int block = slot4(lane & 3, lane >> 2);
+  auto copy_stage = [&](const uint32_t* rows, int s, int to) {
+    const int b = min(4 * s + block, blocks - 1);
+    unrolled<kCopies>([&](auto c) {
+      copy16(codes + 16 * static_cast<uint64_t>(rows[c] + b), lds + to * kStage + 1024 * (kCopies * wave + c));
+    });
+  };
+
+  // Scales of 32 blocks from 32 S on: piece l % 4 of a row is 8 bytes, its last
+  // ones moved to their places where the row ends inside.
+  uint2 sv[kCopies];
+  auto load_scales = [&](const uint32_t* rows, int S) {
+    const int b0 = 32 * S + 8 * (again(lane) & 3);
+    unrolled<kCopies>([&](auto c) {
+      const uint8_t* p = powers + rows[c];
+      if (b0 + 8 <= blocks) {
+        sv[c] = ld8_any(p + b0);
+      } else if (b0 < blocks) {
+        uint64_t v = 0;
+        if (blocks >= 8) {
+          const uint2 d = ld8_any(p + blocks - 8);
+          v = (d.x | static_cast<uint64_t>(d.y) << 32) >> (8 * (b0 + 8 - blocks));
+        } else {
+          for (int i = 0; i < blocks - b0; ++i) v |= static_cast<uint64_t>(p[b0 + i]) << (8 * i);
+        }
+        sv[c] = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+      }
+    });
+  };
+  // Bytes g and 4 + g of a piece are two stages of lanes of quarter g.
+  auto keep_scales = [&]() {
+    const int lane = again(threadIdx.x & 63);
+    unrolled<kCopies>([&](auto c) {
+      const int t = 16 * (kCopies * wave + c) + (lane >> 2), piece = lane & 3;
+      uint8_t* to = &scales[32 * t + 4 * ((piece >> 1) ^ (t >> 3 & 1)) + 2 * (piece & 1)];
+      const uint32_t lo = __builtin_amdgcn_perm(sv[c].y, sv[c].x, 0x05010400);
+      const uint32_t hi = __builtin_amdgcn_perm(sv[c].y, sv[c].x, 0x07030602);
+      *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(lo);
+      *reinterpret_cast<uint16_t*>(to + 8) = static_cast<uint16_t>(lo >> 16);
+      *reinterpret_cast<uint16_t*>(to + 16) = static_cast<uint16_t>(hi);
+      *reinterpret_cast<uint16_t*>(to + 24) = static_cast<uint16_t>(hi >> 16);
+    });
+    __asm__ __volatile__("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+
+  const int lane_at = 64 * r + 16 * slot4(g, r);
+  v4f_t acc[TN][TM];
+  uint4 wf[TN + kAhead], xf[TM], xn[TM];
+  uint32_t sa[TN], sb[TM], sbn[TM];
+  int base = 0;  // the ring's place of the tile's first stage
+  auto read_w = [&](int s, int i) {
+    return *reinterpret_cast<const uint4*>(&ring[((base + s) & 3) * kStage + 1024 * (wn * TN + i) + lane_at]);
+  };
+  auto read_x = [&](int s, int j) {
+    return *reinterpret_cast<const uint4*>(&ring[((base + s) & 3) * kStage + 64 * BN + 1024 * (wm * TM + j) + lane_at]);
+  };
+  // scales of four stages from s on: byte j for stage s + j
+  auto read_scale = [&](int s, int t) {
+    return *reinterpret_cast<const uint32_t*>(&scales[32 * (t + r) + 8 * g + 4 * ((s >> 2 & 1) ^ (r >> 3))]);
+  };
+
+  bool has_next = false;
+  const bool ahead = stages >= 4;  // tiles of fewer stages begin only when the one before has ended
+  auto stage = [&](auto quarter, int s) {
+    // (the next tile's first two stages came before this tile's results left)
+    if (s + 2 < stages || has_next)
+      __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+    else
+      __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    __asm__ __volatile__("s_barrier" ::: "memory");
+    if constexpr (quarter == 1) {
+      if ((s & 4) && s + 3 < stages) keep_scales();  // read from stage s + 2 on
+    }
+    if (s + 3 < stages)
+      copy_stage(first, s + 3, (base + s + 3) & 3);
+    else if (has_next)
+      copy_stage(next_first, s + 3 - stages, (base + s + 3) & 3);
+    if constexpr (quarter == 2) {
+      if (!(s & 4) && s + 6 < stages) load_scales(first, (s >> 3) + 1);
+    }
+    if (4 * s + 4 > blocks) {  // past the row's end: a zero factor
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        if (4 * s + g >= blocks) xf[j] = make_uint4(0, 0, 0, 0);
+    }
+    unrolled<TN>([&](auto i) {
+      if constexpr (i + kAhead < TN)
+        wf[i + kAhead] = read_w(s, i + kAhead);
+      else
+        wf[i + kAhead] = read_w(s + 1, i + kAhead - TN);
+      if constexpr (i >= TN - TM) xn[i - (TN - TM)] = read_x(s + 1, i - (TN - TM));
+      if constexpr (quarter == 3 && i < TM) sbn[i] = read_scale(s + 1, BN + 16 * (wm * TM + i));
+      unrolled<TM>([&](auto j) { acc[i][j] = mfma4s<quarter, quarter>(wf[i], xf[j], acc[i][j], sa[i], sb[j]); });
+      if constexpr (quarter == 3) sa[i] = read_scale(s + 1, 16 * (wn * TN + i));
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int j = 0; j < TM; ++j) xf[j] = xn[j];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) wf[i] = wf[TN + i];
+    if constexpr (quarter == 3) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) sb[j] = sbn[j];
+    }
+  };
+
+  bool begun = false;  // the tile's first stages and scales are on their way
+  for (;;) {
+    if (!begun) {
+      find_rows(tile);
+      find_blocks(tile);
+      load_scales(next_first, 0);
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+        if (s < stages) copy_stage(next_first, s, (base + s) & 3);
+      keep_scales();
+    }
+    none = next_none;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) first[c] = next_first[c];
     __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
-    if (s + 1 < stages) {
-      copy_stage(s + 1);
-      load_scales(s + 1);
-    }
-    const uint8_t* buf = tile[s & 1];
-    const bool tail = 8 * s + 8 > blocks;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = 16 * ((4 * h + g) ^ ((r >> 1) & 7));
-      uint32_t sa[TN / kQuad], sb[TM / kQuad];
-      uint4 xb[TM];
+    for (int j = 0; j < TM; ++j) xf[j] = read_x(0, j), sb[j] = read_scale(0, BN + 16 * (wm * TM + j));
 #pragma unroll
-      for (int i = 0; i < TN / kQuad; ++i) sa[i] = scales[s & 1][4 * h + g][wn * (TN / kQuad) + i][r];
+    for (int i = 0; i < TN; ++i) sa[i] = read_scale(0, 16 * (wn * TN + i));
 #pragma unroll
-      for (int j = 0; j < TM / kQuad; ++j) sb[j] = scales[s & 1][4 * h + g][BN / 16 / kQuad + wm * (TM / kQuad) + j][r];
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        xb[j] = *reinterpret_cast<const uint4*>(buf + (BN + 16 * (wm * TM + j) + r) * 128 + slot);
-        if (tail && 8 * s + 4 * h + g >= blocks) xb[j] = make_uint4(0, 0, 0, 0);  // past the row: a zero factor
-      }
-      unrolled<TN>([&](auto i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(buf + (16 * (wn * TN + i) + r) * 128 + slot);
-        unrolled<TM>([&](auto j) {
-          acc[i][j] = mfma4s<i % kQuad, j % kQuad>(w, xb[j], acc[i][j], sa[i / kQuad], sb[j / kQuad]);
-        });
-      });
-    }
-  }
-
-  // Lane (r, q): activation row 16 j + r of the wave's, neighbouring outputs.
-  constexpr int kOuts = GLU ? 2 * TN : 4 * TN;
-  const int n0 = (GLU ? tn * (BN / 2) + wn * (8 * TN) : tn * BN + wn * (16 * TN)) + g * kOuts;
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int yr = row + 16 * (wm * TM + j) + r;
-    if (yr >= end || n0 >= a.n) continue;
-    float v[kOuts];
+    for (int i = 0; i < kAhead; ++i) wf[i] = read_w(0, i);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if constexpr (GLU) {
-          if (i & 1) v[(i >> 1) * 4 + c] = silu_mul(acc[i - 1][j][c], acc[i][j][c]);
+      for (int j = 0; j < TM; ++j) acc[i][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+    at += step;
+    const bool more = at < run_end;
+    has_next = more && ahead;
+    if (more) next = tiles.at(a, at);
+    // (the next tile's rows are looked up once this one's loads are under way)
+    const int look = stages >= 12 ? 4 : 0, number = stages >= 12 ? 8 : 0;
+    for (int s = 0; s < stages; s += 4) {
+      if (has_next) {
+        if (s == look) find_rows(next);
+        if (s == number) find_blocks(next);
+        if (s + 4 >= stages) load_scales(next_first, 0);
+      }
+      stage(std::integral_constant<int, 0>{}, s);
+      if (s + 1 < stages) stage(std::integral_constant<int, 1>{}, s + 1);
+      if (s + 2 < stages) stage(std::integral_constant<int, 2>{}, s + 2);
+      if (s + 3 < stages) stage(std::integral_constant<int, 3>{}, s + 3);
+    }
+    // all waves have read the last stage and the scales
+    __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+    if (has_next) keep_scales();
+    base = (base + stages) & 3;
+
+    // Results, 16 rows by 256 bytes at a time, through the wave's share of the
+    // ring's free stage, so that a store instruction writes four whole pieces of
+    // 256 bytes.  Lane (r, g) holds activation row 16 j + r and, of a group or
+    // (16-bit outputs) two, neighbours of 16 bytes.
+    constexpr int kSize = OUT == QMV_F32 ? 4 : 2, kPer = 16 / kSize, kEach = kPer / 4;
+    constexpr int kGroups = GLU ? TN / 2 : TN, kRowBytes = kOuts * kSize < 256 ? kOuts * kSize : 256;
+    constexpr int kTurns = kOuts * kSize / kRowBytes, kTurn = kGroups / kTurns, kChunks = kRowBytes / 16;
+    static_assert(kTurn % kEach == 0 && kChunks >= 4 && 16 * kRowBytes <= 4096, "a turn's rows fit a wave's share");
+    uint8_t* out = &ring[((base + 3) & 3) * kStage + 4096 * wave];
+    const int lane = again(threadIdx.x & 63), r = lane & 15, g = lane >> 4;
+    unrolled<TM * kTurns>([&](auto turn) {
+      constexpr int j = turn / kTurns, p0 = turn % kTurns * kTurn;
+      const bool zero = none >> j & 1;
+#pragma unroll
+      for (int p = 0; p < kTurn; p += kEach) {
+        float v[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+          const int i = p0 + p + c / 4;
+          if constexpr (GLU)
+            v[c] = silu_mul(acc[2 * i][j][c % 4], acc[2 * i + 1][j][c % 4]);
+          else
+            v[c] = acc[i][j][c % 4];
+          v[c] = zero ? 0.f : v[c];
+        }
+        uint4 d;
+        if constexpr (OUT == QMV_F32)
+          d = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else if constexpr (OUT == QMV_F16)
+          d = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+        else
+          d = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        const int chunk = place<OUT>(p, g) / kPer;
+        *reinterpret_cast<uint4*>(out + r * kRowBytes + 16 * ((chunk ^ r) & (kChunks - 1))) = d;
+      }
+      __asm__ __volatile__("s_waitcnt lgkmcnt(0)" ::: "memory");
+      constexpr int kLines = 64 / kChunks;  // rows of a store instruction
+#pragma unroll
+      for (int i = 0; i < 16 / kLines; ++i) {
+        const int o = i * kLines + lane / kChunks, chunk = lane % kChunks;
+        const int yr = tile.row + 16 * (wm * TM + j) + o;
+        const int n = tile.tn * (WN * kOuts) + wn * kOuts + place<OUT>(p0, 0) + chunk * kPer;
+        const uint4 d = *reinterpret_cast<const uint4*>(out + o * kRowBytes + 16 * ((chunk ^ o) & (kChunks - 1)));
+        if (yr >= tile.end || n >= a.n) continue;
+        uint8_t* y = static_cast<uint8_t*>(a.y) + (yr * a.y_row + n) * kSize;
+        if (n + kPer <= a.n) {
+          __builtin_nontemporal_store(u32x4_a2{d.x, d.y, d.z, d.w}, reinterpret_cast<u32x4_a2*>(y));
         } else {
-          v[i * 4 + c] = acc[i][j][c];
+          const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int c = 0; c < kPer; ++c)
+            if (n + c < a.n) {
+              if constexpr (kSize == 4)
+                reinterpret_cast<uint32_t*>(y)[c] = w[c];
+              else
+                reinterpret_cast<uint16_t*>(y)[c] = static_cast<uint16_t>(w[c / 2] >> (16 * (c & 1)));
+            }
         }
       }
-    if (a.x_index && (a.x_index[yr] < 0 || a.x_index[yr] >= a.x_rows)) {
-#pragma unroll
-      for (int i = 0; i < kOuts; ++i) v[i] = 0.f;
-    }
-    const int64_t at = yr * a.y_row + n0;
-    if (n0 + kOuts <= a.n) {
-      store_many<OUT, kOuts>(a.y, at, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kOuts; ++i)
-        if (n0 + i < a.n) store_one<OUT>(a.y, at + i, v[i]);
-    }
+      __asm__ __volatile__("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next turn's writes
+    });
+    if (!more) return;
+    tile = next;
+    begun = has_next;
+    if (!begun) lds_barrier();  // everybody's results are out of the ring
   }
 }
 
@@ -403,7 +605,9 @@ template <int WN, int WM, int TN, int TM, int OUT, bool GLU>
 static hipError_t launch_tile(const Mx4Launch& a, hipStream_t s) {
   constexpr int outs = 16 * WN * TN / (GLU ? 2 : 1);
   const int64_t tiles_n = (static_cast<int64_t>(a.n) + outs - 1) / outs, tiles_m = most_tiles(a, 16 * WM * TM);
-  hipLaunchKernelGGL((mx4_tile_kernel<WN, WM, TN, TM, OUT, GLU>), dim3(static_cast<unsigned>(tiles_m * tiles_n)),
+  const int64_t held = static_cast<int64_t>(device_cus()) * (WN * WM == 8 ? 1 : 2);
+  const int64_t grid = (std::min(tiles_m * tiles_n, held) + 7) / 8 * 8;  // each XCD's workgroups share its run
+  hipLaunchKernelGGL((mx4_tile_kernel<WN, WM, TN, TM, OUT, GLU>), dim3(static_cast<unsigned>(grid)),
                      dim3(64 * WN * WM), 0, s, a, static_cast<int>(tiles_n));
   return hipGetLastError();
 }
@@ -415,7 +619,7 @@ static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
   if (per > 32) return launch_tile<2, 2, 4, 4, OUT, GLU>(a, s);
   const int64_t tiles_n = (static_cast<int64_t>(a.n) + (GLU ? 15 : 31)) / (GLU ? 16 : 32);
   const int64_t tiles_m = most_tiles(a, 16);
-  hipLaunchKernelGGL((mx4_stream_kernel<1, OUT, GLU>), dim3(static_cast<unsigned>(tiles_m * tiles_n)), dim3(256), 0, s, a,
+  hipLaunchKernelGGL((mx4_stream_kernel<1, OUT, GLU>), dim3(static_cast<unsigned>((tiles_m * tiles_n + 7) / 8 * 8)), dim3(256), 0, s, a,
                      static_cast<int>(tiles_n));
   return hipGetLastError();
 }
