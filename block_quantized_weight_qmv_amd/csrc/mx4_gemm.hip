@@ -8,7 +8,10 @@
 // codes go from memory to the instruction as they are.  A product of two codes
 // is exact, sums are fp32.  Weights are the A operand, activations B: a lane's
 // four results are four consecutive outputs of one activation row.
+#include <math.h>
+
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "launch.h"
@@ -173,91 +176,6 @@ __device__ __forceinline__ void store_many(void* y, int64_t at, const float* v) 
   }
 }
 
-// Few activation rows: 16 MT of them against 32 weight rows (with GLU 16 of the
-// gate and the same 16 of up) to a workgroup, whose four waves share the
-// columns (every fourth piece of 512) and add their sums in LDS.
-template <int MT, int OUT, bool GLU>
-__global__ void __launch_bounds__(256)
-mx4_stream_kernel(const Mx4Launch a, int tiles_n) {
-  __shared__ float part[4][2 * MT * 4][64];
-  Tiles tiles;
-  tiles.init(a, 16 * MT, tiles_n);
-  int first, run_end;
-  tiles.run(first, run_end);
-  first += blockIdx.x >> 3;
-  if (first >= run_end) return;
-  const Tile at = tiles.at(a, first);
-  const int e = at.e, row = at.row, end = at.end, tn = at.tn;
-  const int lane = __lane_id(), wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int blocks = a.k / 32;
-  const int64_t kc = a.k / 2;
-  // rows of the two weight tiles and of the activation tiles (past the end: the last one again, not stored)
-  const uint8_t *wc[2], *wp[2], *xc[MT], *xp[MT];
-  const int64_t base = static_cast<int64_t>(e) * (GLU ? 2 : 1) * a.n;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int64_t j = base + (GLU ? min(16 * tn + r, a.n - 1) + t * a.n : min(32 * tn + 16 * t + r, a.n - 1));
-    wc[t] = a.w + j * kc;
-    wp[t] = a.ws + j * blocks;
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int i = min(row + 16 * t + r, end - 1);
-    int64_t j = a.x_index ? a.x_index[i] : i;
-    if (j < 0 || j >= a.x_rows) j = 0;  // (such a row's outputs are zeros below)
-    xc[t] = a.x + j * kc;
-    xp[t] = a.xs + j * blocks;
-  }
-  v4f_t acc[2][MT];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = v4f_t{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = 4 * wave; b0 < blocks; b0 += 16) {  // 128 columns: block b0 + g of each lane's row
-    const int b = min(b0 + g, blocks - 1);
-    uint4 wv[2], xv[MT];
-    uint32_t wq[2], xq[MT];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      wv[t] = ld16(wc[t] + 16 * b);
-      wq[t] = wp[t][b];
-      if (b0 + g >= blocks) wv[t] = make_uint4(0, 0, 0, 0);  // past the row: a zero factor
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      xv[m] = ld16(xc[m] + 16 * b);
-      xq[m] = xp[m][b];
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[t][m] = mfma4(wv[t], xv[m], acc[t][m], wq[t], xq[m]);
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][(t * MT + m) * 4 + i][lane] = acc[t][m][i];
-  __syncthreads();
-  // a wave joins a quarter of the results
-  for (int j = wave; j < (GLU ? 1 : 2) * MT * 4; j += 4) {
-    float v = 0.f, u = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v += part[w][j][lane];
-    const int m = j / 4 % MT, i = j & 3, t = j / (4 * MT);
-    const int yr = row + 16 * m + r, col = (GLU ? 16 : 32) * tn + 16 * t + 4 * g + i;
-    if constexpr (GLU) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) u += part[w][j + 4 * MT][lane];
-      v = silu_mul(v, u);
-    }
-    if (yr >= end || col >= a.n) continue;
-    if (a.x_index && (a.x_index[yr] < 0 || a.x_index[yr] >= a.x_rows)) v = 0.f;
-    store_one<OUT>(a.y, yr * a.y_row + col, v);
-  }
-}
-
 template <int N, class F>
 __device__ __forceinline__ void unrolled(F f) {
   if constexpr (N > 0) {
@@ -274,12 +192,123 @@ __device__ __forceinline__ v4f_t mfma4s(const uint4& a, const uint4& b, v4f_t c,
                                                           static_cast<int>(sb));
 }
 
-// 16 bytes of each lane from memory to LDS at `lds` + 16 x lane.  (The s_nop
-// covers an M0 or address written just before, which the compiler cannot see
+// 16 bytes of each lane, from base + off, to LDS at `lds` + 16 x lane.  (The s_nop
+// covers an M0, base or offset written just before, which the compiler cannot see
 // being used here; waits and barriers that no memory access crosses keep LDS
 // reads apart from the copies.)
-__device__ __forceinline__ void copy16(const uint8_t* src, uint32_t lds) {
-  __asm__ __volatile__("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(lds) : "m0");
+__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t off, uint32_t lds) {
+  __asm__ __volatile__("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(lds) : "m0");
+}
+
+// Eight scale bytes of a row from block b on (a multiple of eight before its
+// end; bytes past the end are anything), at any alignment and within the row.
+__device__ __forceinline__ uint2 scales8(const uint8_t* p, int b, int blocks) {
+  if (b + 8 <= blocks) return ld8_any(p + b);
+  uint64_t v = 0;
+  if (blocks >= 8) {
+    const uint2 d = ld8_any(p + blocks - 8);
+    v = (d.x | static_cast<uint64_t>(d.y) << 32) >> (8 * (b + 8 - blocks));
+  } else {
+    for (int i = 0; i < blocks - b; ++i) v |= static_cast<uint64_t>(p[b + i]) << (8 * i);
+  }
+  return make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+}
+
+// Few activation rows: 16 MT of them against 16 NT weight rows (with GLU every
+// other sixteen of the gate and of up) to a workgroup.  Its W waves take every
+// W-th piece of 256 columns (a whole line of every row) and add their sums in
+// LDS.  Fragments go from memory to the matrix instruction without LDS, D
+// pieces of a wave ahead: the weights' bytes bound it, and what is in flight
+// decides how near it comes.
+template <int NT, int MT, int W, int D, int OUT, bool GLU>
+__global__ void __launch_bounds__(64 * W)
+mx4_stream_kernel(const Mx4Launch a, int tiles_n) {
+  constexpr int kOuts = 16 * NT / (GLU ? 2 : 1);
+  __shared__ float part[W][NT * MT * 4][64];
+  Tiles tiles;
+  tiles.init(a, 16 * MT, tiles_n);
+  int first, run_end;
+  tiles.run(first, run_end);
+  first += blockIdx.x >> 3;
+  if (first >= run_end) return;
+  const Tile at = tiles.at(a, first);
+  const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int blocks = a.k / 32, pieces = (blocks + 7) / 8;
+  // rows of the weight tiles, then of the activation tiles (past the end: the last one again, not stored)
+  const uint8_t *codes[NT + MT], *powers[NT + MT];
+  const int64_t base = static_cast<int64_t>(at.e) * (GLU ? 2 : 1) * a.n;
+  unrolled<NT + MT>([&](auto t) {
+    int64_t j;
+    if constexpr (t < NT) {
+      const int n = at.tn * kOuts + 16 * (GLU ? t / 2 : t) + r;
+      j = base + min(n, a.n - 1) + (GLU && (t & 1) ? a.n : 0);
+    } else {
+      const int i = min(at.row + 16 * (t - NT) + r, at.end - 1);
+      j = a.x_index ? a.x_index[i] : i;
+      if (j < 0 || j >= a.x_rows) j = 0;  // (such a row's outputs are zeros below)
+    }
+    codes[t] = (t < NT ? a.w : a.x) + j * blocks * 16;
+    powers[t] = (t < NT ? a.ws : a.xs) + j * blocks;
+  });
+  v4f_t acc[NT][MT];
+  unrolled<NT>([&](auto t) { unrolled<MT>([&](auto m) { acc[t][m] = v4f_t{0.f, 0.f, 0.f, 0.f}; }); });
+  struct Piece {
+    uint4 c[NT + MT][2];
+    uint2 p[NT + MT];
+  } f[D];
+  auto load = [&](Piece& f, int u) {  // blocks 8 u + g and 8 u + 4 + g of each lane's row (past the last: that one)
+    unrolled<NT + MT>([&](auto t) {
+      f.c[t][0] = ld16(codes[t] + 16 * static_cast<int64_t>(min(8 * u + g, blocks - 1)));
+      f.c[t][1] = ld16(codes[t] + 16 * static_cast<int64_t>(min(8 * u + 4 + g, blocks - 1)));
+    });
+    unrolled<NT + MT>([&](auto t) { f.p[t] = scales8(powers[t], 8 * u, blocks); });
+  };
+  unrolled<D>([&](auto d) {
+    if (wave + d * W < pieces) load(f[d], wave + d * W);
+  });
+  for (int u0 = wave; u0 < pieces; u0 += D * W) {
+    unrolled<D>([&](auto d) {
+      const int u = u0 + d * W;
+      if (u >= pieces) return;
+      if (8 * u + 8 > blocks) {  // past the row's end: a zero factor
+        unrolled<MT>([&](auto m) {
+          if (8 * u + g >= blocks) f[d].c[NT + m][0] = make_uint4(0, 0, 0, 0);
+          if (8 * u + 4 + g >= blocks) f[d].c[NT + m][1] = make_uint4(0, 0, 0, 0);
+        });
+      }
+      unrolled<2>([&](auto h) {
+        uint32_t p[NT + MT];
+        unrolled<NT + MT>([&](auto t) { p[t] = (h ? f[d].p[t].y : f[d].p[t].x) >> (8 * g); });
+        unrolled<NT>([&](auto t) {
+          unrolled<MT>([&](auto m) { acc[t][m] = mfma4(f[d].c[t][h], f[d].c[NT + m][h], acc[t][m], p[t], p[NT + m]); });
+        });
+      });
+      if (u + D * W < pieces) load(f[d], u + D * W);
+    });
+  }
+  unrolled<NT>([&](auto t) {
+    unrolled<MT>([&](auto m) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[wave][(t * MT + m) * 4 + i][lane] = acc[t][m][i];
+    });
+  });
+  __syncthreads();
+  // the waves share the results
+  constexpr int kResults = (GLU ? NT / 2 : NT) * MT * 4;
+  for (int j = wave; j < kResults; j += W) {
+    const int i = j & 3, m = j / 4 % MT, t = j / (4 * MT);
+    auto sum = [&](int of) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += part[w][(of * MT + m) * 4 + i][lane];
+      return v;
+    };
+    const int yr = at.row + 16 * m + r, col = at.tn * kOuts + 16 * t + 4 * g + i;
+    float v = GLU ? silu_mul(sum(2 * t), sum(2 * t + 1)) : sum(t);
+    if (yr >= at.end || col >= a.n) continue;
+    if (a.x_index && (a.x_index[yr] < 0 || a.x_index[yr] >= a.x_rows)) v = 0.f;
+    store_one<OUT>(a.y, yr * a.y_row + col, v);
+  }
 }
 
 // The first of the four outputs that lane quarter q holds of group p, among
@@ -301,10 +330,10 @@ __device__ __forceinline__ int slot4(int piece, int r) { return piece ^ (0x78 >>
 // ring of four: while stage s is multiplied, stage s + 1 is read into registers
 // two fragments ahead of its use, and s + 2 and s + 3 are on their way.  One
 // barrier a stage says both that stage s + 1 has come and that stage s - 1 is
-// read.  Scales take another way (a row's are too few bytes, at any alignment,
-// for copies): 64 blocks' bytes of each row are loaded by four lanes, turned so
-// that a lane's four stages are a dword, and kept in LDS; the matrix
-// instruction picks the stage's byte.
+// read.  Scales take another way (a row's are few bytes, at any alignment): 32
+// blocks' bytes of each row are loaded by four lanes, turned so that a lane's
+// four stages are a dword, and kept in LDS; the matrix instruction picks the
+// stage's byte.
 //
 // A workgroup stays for as many tiles as there are (grid = what the GPU holds):
 // the next tile's first stages, and its scales, are loaded while this one's
@@ -316,7 +345,7 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
   constexpr int kCopies = kRows / 16 / kWaves;  // a wave's copy instructions of a stage: 16 rows x 64 bytes each
   constexpr int kOuts = 16 * TN / (GLU ? 2 : 1);  // outputs of a wave's rows
   constexpr int kAhead = 2;                       // weight fragments read ahead of their use
-  static_assert(kRows % (16 * kWaves) == 0 && kStage / kWaves == 4096, "whole copies; 4 KB of a stage to a wave");
+  static_assert(kRows == 64 * kWaves, "whole copies, and 4 KB of a stage, to a wave");
   __shared__ __attribute__((aligned(128))) uint8_t ring[4 * kStage];
   __shared__ __attribute__((aligned(128))) uint8_t scales[kRows * 32];
   const int lane = __lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -336,7 +365,7 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
   auto weight_row = [&](const Tile& to, int t) {
     const int w = t / (16 * TN), gr = t / 16 % TN, q = t / 4 & 3, i = t & 3;
     const int n = to.tn * (WN * kOuts) + w * kOuts + place<OUT>(GLU ? gr >> 1 : gr, q) + i;
-    return static_cast<uint32_t>((to.e * (GLU ? 2 : 1) + (GLU ? gr & 1 : 0)) * a.n + min(n, a.n - 1));
+    return (GLU ? gr & 1 : 0) * a.n + min(n, a.n - 1);
   };
   auto activation_row = [&](int i) {  // (past the group's end: its last row again, not stored)
     const int j = a.x_index ? a.x_index[i] : i;
@@ -344,17 +373,20 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
   };
 
   // Lane l of copy c serves row 16 (kCopies wave + c) + l / 4, piece l % 4.  A
-  // row is known by its first block's number: 16 bytes of codes, one of scale.
+  // row is known by its bytes from the start of its expert's codes, or of the
+  // activations' (a sixteenth of that in the scales).
   const bool weights = wave < BN / 16 / kCopies;  // this wave copies weight rows, or activation rows
-  const uint8_t* codes = weights ? a.w : a.x;
-  const uint8_t* powers = weights ? a.ws : a.xs;
-  uint32_t first[kCopies], next_first[kCopies];
+  const int64_t matrix = static_cast<int64_t>(GLU ? 2 : 1) * a.n * blocks;  // blocks of an expert's matrix
+  struct Source {
+    const uint8_t *codes, *powers;
+    uint32_t row[kCopies];
+  } from, next_from;
   uint32_t none = 0, next_none = 0;  // bit j: this lane's activation row 16 j + r has no index
   auto find_rows = [&](const Tile& to) {
     const int lane = again(threadIdx.x & 63), r = lane & 15;
     unrolled<kCopies>([&](auto c) {
       const int t = 16 * (kCopies * wave + c) + (lane >> 2);
-      next_first[c] = weights ? 0 : max(activation_row(min(to.row + t - BN, to.end - 1)), 0);
+      next_from.row[c] = weights ? 0 : max(activation_row(min(to.row + t - BN, to.end - 1)), 0);
     });
     next_none = 0;
     if (a.x_index) {
@@ -367,37 +399,25 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
     const int lane = again(threadIdx.x & 63);
     unrolled<kCopies>([&](auto c) {
       const int t = 16 * (kCopies * wave + c) + (lane >> 2);
-      next_first[c] = (weights ? weight_row(to, t) : next_first[c]) * static_cast<uint32_t>(blocks);
+      next_from.row[c] = (weights ? weight_row(to, t) : next_from.row[c]) * static_cast<uint32_t>(blocks) * 16;
     });
+    next_from.codes = weights ? a.w + 16 * (to.e * matrix) : a.x;
+    next_from.powers = weights ? a.ws + to.e * matrix : a.xs;
   };
   const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(&ring[0]));
   const int block = slot4(lane & 3, lane >> 2);
-  auto copy_stage = [&](const uint32_t* rows, int s, int to) {
-    const int b = min(4 * s + block, blocks - 1);
-    unrolled<kCopies>([&](auto c) {
-      copy16(codes + 16 * static_cast<uint64_t>(rows[c] + b), lds + to * kStage + 1024 * (kCopies * wave + c));
-    });
+  auto copy_stage = [&](const Source& f, int s, int to) {
+    const uint32_t off = 16 * min(4 * s + block, blocks - 1);
+    unrolled<kCopies>([&](auto c) { copy16(f.codes, f.row[c] + off, lds + to * kStage + 1024 * (kCopies * wave + c)); });
   };
 
   // Scales of 32 blocks from 32 S on: piece l % 4 of a row is 8 bytes, its last
   // ones moved to their places where the row ends inside.
   uint2 sv[kCopies];
-  auto load_scales = [&](const uint32_t* rows, int S) {
+  auto load_scales = [&](const Source& f, int S) {
     const int b0 = 32 * S + 8 * (again(lane) & 3);
     unrolled<kCopies>([&](auto c) {
-      const uint8_t* p = powers + rows[c];
-      if (b0 + 8 <= blocks) {
-        sv[c] = ld8_any(p + b0);
-      } else if (b0 < blocks) {
-        uint64_t v = 0;
-        if (blocks >= 8) {
-          const uint2 d = ld8_any(p + blocks - 8);
-          v = (d.x | static_cast<uint64_t>(d.y) << 32) >> (8 * (b0 + 8 - blocks));
-        } else {
-          for (int i = 0; i < blocks - b0; ++i) v |= static_cast<uint64_t>(p[b0 + i]) << (8 * i);
-        }
-        sv[c] = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
-      }
+      if (b0 < blocks) sv[c] = scales8(f.powers + (f.row[c] >> 4), b0, blocks);
     });
   };
   // Bytes g and 4 + g of a piece are two stages of lanes of quarter g.
@@ -418,7 +438,7 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
 
   const int lane_at = 64 * r + 16 * slot4(g, r);
   v4f_t acc[TN][TM];
-  uint4 wf[TN + kAhead], xf[TM], xn[TM];
+  uint4 wf[TN + kAhead], xf[2][TM];  // activations of even and odd stages
   uint32_t sa[TN], sb[TM], sbn[TM];
   int base = 0;  // the ring's place of the tile's first stage
   auto read_w = [&](int s, int i) {
@@ -428,47 +448,45 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
     return *reinterpret_cast<const uint4*>(&ring[((base + s) & 3) * kStage + 64 * BN + 1024 * (wm * TM + j) + lane_at]);
   };
   // scales of four stages from s on: byte j for stage s + j
-  auto read_scale = [&](int s, int t) {
+  auto read_scale = [&](int s, int t) -> uint32_t {
     return *reinterpret_cast<const uint32_t*>(&scales[32 * (t + r) + 8 * g + 4 * ((s >> 2 & 1) ^ (r >> 3))]);
   };
 
+  bool begun = false;  // the tile's first stages and scales came while the one before was worked on
+  int ahead_of = 0, wait_from = 0;  // stages that copies are ahead of; the first stage that waits
+  const int tail = (blocks & 3) ? stages - 1 : -1;
   bool has_next = false;
   const bool ahead = stages >= 4;  // tiles of fewer stages begin only when the one before has ended
   auto stage = [&](auto quarter, int s) {
-    // (the next tile's first two stages came before this tile's results left)
-    if (s + 2 < stages || has_next)
-      __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
-    else
-      __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
+    // (a tile begun ahead has its first three stages, and the results of the
+    // one before may still be leaving)
+    if (quarter >= 2 || s >= wait_from) __asm__ __volatile__("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
     __asm__ __volatile__("s_barrier" ::: "memory");
     if constexpr (quarter == 1) {
       if ((s & 4) && s + 3 < stages) keep_scales();  // read from stage s + 2 on
     }
-    if (s + 3 < stages)
-      copy_stage(first, s + 3, (base + s + 3) & 3);
-    else if (has_next)
-      copy_stage(next_first, s + 3 - stages, (base + s + 3) & 3);
+    if (s + 3 == stages && has_next) from = next_from, ahead_of = stages;
+    // (after the last tile's last stage: its last blocks again, read by nobody)
+    copy_stage(from, s + 3 - ahead_of, (base + s + 3) & 3);
     if constexpr (quarter == 2) {
-      if (!(s & 4) && s + 6 < stages) load_scales(first, (s >> 3) + 1);
+      if (!(s & 4) && s + 6 < stages) load_scales(from, (s >> 3) + 1);
     }
-    if (4 * s + 4 > blocks) {  // past the row's end: a zero factor
+    if (s == tail) {  // the row ends inside: a zero factor behind its end
 #pragma unroll
       for (int j = 0; j < TM; ++j)
-        if (4 * s + g >= blocks) xf[j] = make_uint4(0, 0, 0, 0);
+        if (4 * s + g >= blocks) xf[quarter & 1][j] = make_uint4(0, 0, 0, 0);
     }
     unrolled<TN>([&](auto i) {
       if constexpr (i + kAhead < TN)
         wf[i + kAhead] = read_w(s, i + kAhead);
       else
         wf[i + kAhead] = read_w(s + 1, i + kAhead - TN);
-      if constexpr (i >= TN - TM) xn[i - (TN - TM)] = read_x(s + 1, i - (TN - TM));
-      if constexpr (quarter == 3 && i < TM) sbn[i] = read_scale(s + 1, BN + 16 * (wm * TM + i));
-      unrolled<TM>([&](auto j) { acc[i][j] = mfma4s<quarter, quarter>(wf[i], xf[j], acc[i][j], sa[i], sb[j]); });
+      if constexpr (i >= TN - TM) xf[~quarter & 1][i - (TN - TM)] = read_x(s + 1, i - (TN - TM));
+      if constexpr ((quarter == 3) && i < TM) sbn[i] = read_scale(s + 1, BN + 16 * (wm * TM + i));
+      unrolled<TM>([&](auto j) { acc[i][j] = mfma4s<quarter, quarter>(wf[i], xf[quarter & 1][j], acc[i][j], sa[i], sb[j]); });
       if constexpr (quarter == 3) sa[i] = read_scale(s + 1, 16 * (wn * TN + i));
       __builtin_amdgcn_sched_barrier(0);
     });
-#pragma unroll
-    for (int j = 0; j < TM; ++j) xf[j] = xn[j];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) wf[i] = wf[TN + i];
     if constexpr (quarter == 3) {
@@ -477,24 +495,23 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
     }
   };
 
-  bool begun = false;  // the tile's first stages and scales are on their way
   for (;;) {
     if (!begun) {
       find_rows(tile);
       find_blocks(tile);
-      load_scales(next_first, 0);
+      load_scales(next_from, 0);
 #pragma unroll
-      for (int s = 0; s < 3; ++s)
-        if (s < stages) copy_stage(next_first, s, (base + s) & 3);
+      for (int s = 0; s < 3; ++s) copy_stage(next_from, s, (base + s) & 3);
       keep_scales();
     }
     none = next_none;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) first[c] = next_first[c];
+    from = next_from;
+    ahead_of = 0;
+    wait_from = begun ? 2 : 0;
     __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
 #pragma unroll
-    for (int j = 0; j < TM; ++j) xf[j] = read_x(0, j), sb[j] = read_scale(0, BN + 16 * (wm * TM + j));
+    for (int j = 0; j < TM; ++j) xf[0][j] = read_x(0, j), sb[j] = read_scale(0, BN + 16 * (wm * TM + j));
 #pragma unroll
     for (int i = 0; i < TN; ++i) sa[i] = read_scale(0, 16 * (wn * TN + i));
 #pragma unroll
@@ -508,12 +525,12 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
     has_next = more && ahead;
     if (more) next = tiles.at(a, at);
     // (the next tile's rows are looked up once this one's loads are under way)
-    const int look = stages >= 12 ? 4 : 0, number = stages >= 12 ? 8 : 0;
+    const int look = stages >= 12 ? 4 : 0, number = 2 * look;
     for (int s = 0; s < stages; s += 4) {
       if (has_next) {
         if (s == look) find_rows(next);
         if (s == number) find_blocks(next);
-        if (s + 4 >= stages) load_scales(next_first, 0);
+        if (s + 4 >= stages) load_scales(next_from, 0);
       }
       stage(std::integral_constant<int, 0>{}, s);
       if (s + 1 < stages) stage(std::integral_constant<int, 1>{}, s + 1);
@@ -601,6 +618,18 @@ static int64_t most_tiles(const Mx4Launch& a, int bm) {
   return whole + std::min(a.experts, a.rows);
 }
 
+// Tiles that rows spread unevenly over the experts are likely to take.
+static double usual_tiles(const Mx4Launch& a, int bm) {
+  if (!a.expert_start) return (a.rows + bm - 1) / bm;
+  const double used = std::min(a.experts, a.rows), each = a.rows / (used * bm);
+  return used * (each <= 0.5 ? 1 : each + 0.5);
+}
+
+// Columns of tiles of 16 nt weight rows.
+static double tiles_n_of(const Mx4Launch& a, bool glu, int nt) {
+  return std::ceil(a.n / (16.0 * nt / (glu ? 2 : 1)));
+}
+
 template <int WN, int WM, int TN, int TM, int OUT, bool GLU>
 static hipError_t launch_tile(const Mx4Launch& a, hipStream_t s) {
   constexpr int outs = 16 * WN * TN / (GLU ? 2 : 1);
@@ -612,16 +641,55 @@ static hipError_t launch_tile(const Mx4Launch& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int OUT, bool GLU>
-static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
-  const int64_t per = a.rows / a.experts;  // rows of a matrix, on average
-  if (per > 512) return launch_tile<2, 4, 8, 4, OUT, GLU>(a, s);
-  if (per > 32) return launch_tile<2, 2, 4, 4, OUT, GLU>(a, s);
-  const int64_t tiles_n = (static_cast<int64_t>(a.n) + (GLU ? 15 : 31)) / (GLU ? 16 : 32);
-  const int64_t tiles_m = most_tiles(a, 16);
-  hipLaunchKernelGGL((mx4_stream_kernel<1, OUT, GLU>), dim3(static_cast<unsigned>((tiles_m * tiles_n + 7) / 8 * 8)), dim3(256), 0, s, a,
+template <int NT, int MT, int W, int D, int OUT, bool GLU>
+static hipError_t launch_stream(const Mx4Launch& a, hipStream_t s) {
+  constexpr int outs = 16 * NT / (GLU ? 2 : 1);
+  const int64_t tiles_n = (static_cast<int64_t>(a.n) + outs - 1) / outs, tiles_m = most_tiles(a, 16 * MT);
+  hipLaunchKernelGGL((mx4_stream_kernel<NT, MT, W, D, OUT, GLU>),
+                     dim3(static_cast<unsigned>((tiles_m * tiles_n + 7) / 8 * 8)), dim3(64 * W), 0, s, a,
                      static_cast<int>(tiles_n));
   return hipGetLastError();
+}
+
+// What a launch of tiles of 16 nt weight rows x 16 mt activation rows is expected
+// to take (us): `each` for every CU's share of them at 3584 columns, one tile's
+// own way at least.
+static double stream_cost(const Mx4Launch& a, bool glu, int nt, int mt, double each, double least) {
+  const double tiles = tiles_n_of(a, glu, nt) * usual_tiles(a, 16 * mt);
+  return 2.5 + a.k / 3584.0 * std::max(least, each * tiles / 256);
+}
+
+template <int OUT, bool GLU>
+static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
+#ifdef FORCE
+  if (FORCE == 0 && !GLU) return launch_stream<GLU ? 2 : 1, 1, 8, 2, OUT, GLU>(a, s);
+  if (FORCE == 2) return launch_stream<2, 2, 8, 2, OUT, GLU>(a, s);
+  if (FORCE == 4) return launch_tile<2, 2, 4, 4, OUT, GLU>(a, s);
+  if (FORCE == 5) return launch_tile<2, 4, 8, 4, OUT, GLU>(a, s);
+  if (FORCE == 6) return launch_stream<2, 4, 8, 1, OUT, GLU>(a, s);
+  if (FORCE == 8) return launch_stream<4, 1, 4, 2, OUT, GLU>(a, s);
+  if (FORCE == 9) return launch_stream<2, 1, 8, 1, OUT, GLU>(a, s);
+#endif
+  // The kernel that is expected to end first.  The figures are measured ones at
+  // 3584 columns: for a stream kernel, time a tile takes of a CU that has several,
+  // and a lone tile's; for the tile kernels, time of one tile on each CU, and
+  // (128 x 128) of two.
+  const double small = tiles_n_of(a, GLU, 8) * usual_tiles(a, 128), large = tiles_n_of(a, GLU, 16) * usual_tiles(a, 256);
+  const double rest = small - 512 * std::floor(small / 512);
+  const double cost[7] = {GLU ? 1e30 : stream_cost(a, GLU, 1, 1, 2.2, 2.0), stream_cost(a, GLU, 2, 1, 3.4, 2.7),
+                          stream_cost(a, GLU, 4, 1, 5.0, 5.0),            stream_cost(a, GLU, 2, 2, 5.8, 3.5),
+                          stream_cost(a, GLU, 2, 4, 9.2, 6.5),
+                          2.5 + a.k / 3584.0 * (20 * std::floor(small / 512) + (rest == 0 ? 0 : rest <= 256 ? 13.3 : 20)),
+                          2.5 + a.k / 3584.0 * 27 * std::max(1.0, large / 256)};
+  switch (std::min_element(cost, cost + 7) - cost) {
+    case 0: return launch_stream<GLU ? 2 : 1, 1, 8, 2, OUT, GLU>(a, s);
+    case 1: return launch_stream<2, 1, 8, 1, OUT, GLU>(a, s);
+    case 2: return launch_stream<4, 1, 4, 2, OUT, GLU>(a, s);
+    case 3: return launch_stream<2, 2, 8, 2, OUT, GLU>(a, s);
+    case 4: return launch_stream<2, 4, 8, 1, OUT, GLU>(a, s);
+    case 5: return launch_tile<2, 2, 4, 4, OUT, GLU>(a, s);
+    default: return launch_tile<2, 4, 8, 4, OUT, GLU>(a, s);
+  }
 }
 
 template <int OUT>
