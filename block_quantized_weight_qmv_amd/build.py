@@ -25,7 +25,7 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 
 HIP_SOURCES = ["api.cpp", "gemv_q8_0.hip", "gemv_q4_k.hip", "gemv_q5_k.hip", "gemv_q6_k.hip",
                "gemv_int4_g128.hip", "gemv_mxfp4.hip", "gemm_q4_k_mfma.hip", "gemm_q4_k_dqreg.hip", "dequant.hip", "repack.hip", "probe.hip",
-               "attn.hip", "verify.hip", "mx4_quant.hip", "mx4_gemm.hip", "norm.hip"]
+               "attn.hip", "verify.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_exact.hip", "norm.hip"]
 CXX_SOURCES = ["packer.cpp"]
 # Per-source device flags.  The matrix-core kernels scale each product in
 # VALU right away; in accumulation registers every result would need a

@@ -263,7 +263,8 @@ static int32_t check_mx4(const qmv_mx4_args* a) {
   for (const qmv_weights* W : {a->W, a->X})
     if (overlap(a->y, bytes, W->data, static_cast<int64_t>(W->nbytes)))
       return fail(QMV_ERR_SHAPE, "y overlaps %s", W == a->W ? "W" : "X");
-  if (!mx4_gemm_fits(*a)) return fail(QMV_ERR_UNSUPPORTED, "more tiles than a launch has workgroups");
+  if (!mx4_gemm_fits(*a))
+    return fail(QMV_ERR_UNSUPPORTED, "more than 2^32 bytes of codes in a matrix or X, or more than 2^28 tiles");
   return QMV_OK;
 }
 
@@ -620,8 +621,17 @@ static int32_t gemv_multi_impl(int32_t fmt, int32_t x_dtype, int64_t batch, cons
     // 27.0 against 25.1 us at three)
     const bool q4k_mfma = fmt == QMV_Q4_K && x_dtype == QMV_BF16 && batch >= qmv::kMfmaMinBatch;
     const bool mfma_split = q4k_mfma && batch > 2;
+    // MXFP4 x fp16/bf16: the matrix cores (18944 x 3584, 8 bf16 rows: 19.5
+    // against 30 us in two passes of four; 3584 x 18944, 3 fp16 rows: 17.6 against
+    // 22.3 in two of two, 8: 22.9 against 44)
+    const int64_t exact_rows = fmt == QMV_MXFP4 && half_x ? qmv::kMx4ExactRows : INT64_MAX;
+    const int64_t exact_wide = fmt == QMV_MXFP4 && half_x ? qmv::kMx4ExactWideRows : INT64_MAX;
+    qmv::GemvCall exact[qmv::kMaxItems];
+    int ne = 0;
     for (int i = 0; i < n; ++i) {
-      if (f16_mfma && qmv::gemm_q4_k_f16_fits(calls[i].W->cols, batch))
+      if (batch >= (calls[i].W->cols <= wave_cols ? exact_rows : exact_wide) && qmv::mx4_exact_fits(calls[i].W->rows, batch))
+        exact[ne++] = calls[i];
+      else if (f16_mfma && qmv::gemm_q4_k_f16_fits(calls[i].W->cols, batch))
         mfma16[nm++] = calls[i];
       else if (calls[i].W->cols <= wave_cols)
         narrow[nn++] = calls[i];
@@ -648,6 +658,7 @@ static int32_t gemv_multi_impl(int32_t fmt, int32_t x_dtype, int64_t batch, cons
     if (wst != QMV_OK || ws.need) return wst;
     if (nn) e = rows(narrow, nn);
     if (e == hipSuccess && ns) e = rows(split, ns);
+    for (int i = 0; e == hipSuccess && i < ne; ++i) e = qmv::mx4_exact(exact[i], x_dtype, batch, s);
     if (e == hipSuccess && nm) e = qmv::gemm_q4_k_mfma_items(mfma16, nm, true, batch, s, wsp);
     if (e == hipSuccess && nw) {
       if (q4k_mfma) {

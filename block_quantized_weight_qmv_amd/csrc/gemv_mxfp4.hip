@@ -80,13 +80,27 @@ struct Mxfp4Policy {
 #pragma unroll
       for (int k = 0; k < 64; ++k) s.v[k] = okh[k / 32] ? s.v[k] * f : 0.f;
     } else {
-      float v[64];
-      x_to_f32<64>(raw, v, static_cast<const XT*>(nullptr));
+      // dword i of the raw row: activations 2i and 2i + 1, as the codes' pairs are
+      auto word = [&](int i) {
+        const uint32_t w = (i & 3) == 0 ? raw[i / 4].x : (i & 3) == 1 ? raw[i / 4].y : (i & 3) == 2 ? raw[i / 4].z : raw[i / 4].w;
+        return okh[i / 16] ? w : 0u;
+      };
+      if constexpr (__is_same(XT, _Float16)) {
+        s.e = 0;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) v[k] = okh[k / 32] ? v[k] : 0.f;
-      s.e = half_scale_exp<XT, 64>(v);
+        for (int i = 0; i < 32; ++i) s.h[i] = __builtin_bit_cast(h2_t, word(i));
+      } else {
+        uint32_t top = 0;  // largest magnitude, as bits
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s.h[i] = h2_t{scaled_f16(v[2 * i], s.e), scaled_f16(v[2 * i + 1], s.e)};
+        for (int i = 0; i < 32; ++i) top = max(top, max((word(i) << 16) & 0x7FFFFFFFu, word(i) & 0x7FFF0000u));
+        const float mx[1] = {__uint_as_float(top)};
+        s.e = half_scale_exp<XT, 1>(mx);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t w = word(i);
+          s.h[i] = h2_t{scaled_f16(__uint_as_float(w << 16), s.e), scaled_f16(__uint_as_float(w & 0xFFFF0000u), s.e)};
+        }
+      }
     }
   }
 

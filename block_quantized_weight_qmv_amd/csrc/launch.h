@@ -68,6 +68,12 @@ hipError_t gemv_q6_k_planes(const GemvCall* calls, int n, int x_dtype, int64_t b
 hipError_t gemv_int4_g128(const GemvCall* calls, int n, int x_dtype, int64_t batch,
                           hipStream_t s);
 hipError_t gemv_mxfp4(const GemvCall* calls, int n, int x_dtype, int64_t batch, hipStream_t s);
+// MXFP4 with kMx4ExactRows fp16/bf16 rows and more, or kMx4ExactWideRows against
+// more columns than a wave's slice: the matrix cores (mx4_exact.hip), where a
+// launch holds the tiles.
+constexpr int64_t kMx4ExactRows = 5, kMx4ExactWideRows = 3;
+bool mx4_exact_fits(int64_t rows, int64_t batch);
+hipError_t mx4_exact(const GemvCall& c, int x_dtype, int64_t batch, hipStream_t s);
 hipError_t gemv_mxfp4_rows(const GemvCall* calls, int n, int x_dtype, int64_t batch, hipStream_t s);
 
 // Two matrices of one format, layout and shape on one activation as one

@@ -656,20 +656,13 @@ static hipError_t launch_stream(const Mx4Launch& a, hipStream_t s) {
 // own way at least.
 static double stream_cost(const Mx4Launch& a, bool glu, int nt, int mt, double each, double least) {
   const double tiles = tiles_n_of(a, glu, nt) * usual_tiles(a, 16 * mt);
+  // (a launch's work-items along x are counted in 32 bits)
+  if (tiles_n_of(a, glu, nt) * most_tiles(a, 16 * mt) >= 1 << 22) return 1e30;
   return 2.5 + a.k / 3584.0 * std::max(least, each * tiles / 256);
 }
 
 template <int OUT, bool GLU>
 static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
-#ifdef FORCE
-  if (FORCE == 0 && !GLU) return launch_stream<GLU ? 2 : 1, 1, 8, 2, OUT, GLU>(a, s);
-  if (FORCE == 2) return launch_stream<2, 2, 8, 2, OUT, GLU>(a, s);
-  if (FORCE == 4) return launch_tile<2, 2, 4, 4, OUT, GLU>(a, s);
-  if (FORCE == 5) return launch_tile<2, 4, 8, 4, OUT, GLU>(a, s);
-  if (FORCE == 6) return launch_stream<2, 4, 8, 1, OUT, GLU>(a, s);
-  if (FORCE == 8) return launch_stream<4, 1, 4, 2, OUT, GLU>(a, s);
-  if (FORCE == 9) return launch_stream<2, 1, 8, 1, OUT, GLU>(a, s);
-#endif
   // The kernel that is expected to end first.  The figures are measured ones at
   // 3584 columns: for a stream kernel, time a tile takes of a CU that has several,
   // and a lone tile's; for the tile kernels, time of one tile on each CU, and
@@ -710,9 +703,13 @@ static Mx4Launch describe(const qmv_mx4_args& m) {
   return a;
 }
 
+// The tile kernels number their tiles, and the bytes of a matrix and of the
+// activations, in 32 bits.
 bool mx4_gemm_fits(const qmv_mx4_args& m) {
   const Mx4Launch a = describe(m);
-  return most_tiles(a, 16) * ((static_cast<int64_t>(a.n) + 15) / 16) < (int64_t{1} << 24);
+  const int64_t row = a.k / 2, matrix = m.W->rows / a.experts * row;
+  return most_tiles(a, 128) * ((static_cast<int64_t>(a.n) + 63) / 64) < (int64_t{1} << 28) &&
+         matrix <= (int64_t{1} << 32) && a.x_rows * row <= (int64_t{1} << 32);
 }
 
 hipError_t mx4_gemm(const qmv_mx4_args& m, hipStream_t s) {

@@ -445,6 +445,8 @@ def qmv_dequant(W: QmvWeights, out, out_dtype, stream=None) -> None:
     _check(lib().qmv_dequant(ctypes.byref(W), _ptr(out), _dtype(out_dtype), _stream(stream, out)))
 
 
+_FLOATS = {"float32": 0, "float16": 1, "bfloat16": 2}
+
 # Element types of the index, mask and number tensors of the step's operators.
 _I32, _I64, _F32 = ("int32",), ("int64", "uint64"), ("float32",)
 
@@ -660,14 +662,14 @@ def qmv_verify(a: QmvVerifyArgs, workspace, workspace_bytes: int, stream=None) -
 def qmv_quantize(W: QmvWeights, x, stream=None) -> None:
     """W = x in W's format (mxfp4), written to the bytes that W describes.  x: a device tensor [W.rows, W.cols] of float32,
     float16 or bfloat16, its rows of any stride."""
-    name = str(getattr(x, "dtype", "")).replace("torch.", "")
-    if name not in ("float32", "float16", "bfloat16"):
-        raise QmvError(-6, f"x: {name or type(x)}, expected a float32, float16 or bfloat16 tensor")
-    _check_view(x, "x", name, 2)
-    if tuple(x.shape) != (W.rows, W.cols):
+    code = _FLOATS.get(_dtype_name(x)) if hasattr(x, "dtype") else None
+    if code is None:
+        raise QmvError(-6, f"x: {getattr(x, 'dtype', type(x))}, expected a float32, float16 or bfloat16 tensor")
+    _check_view(x, "x", _dtype_name(x), 2)
+    if x.shape[0] != W.rows or x.shape[1] != W.cols:
         raise QmvError(-3, f"x: shape {tuple(x.shape)}, expected {(W.rows, W.cols)}")
     _check_with("W", getattr(W, "owner", None), "x", x)
-    _check(lib().qmv_quantize(ctypes.byref(W), x.data_ptr(), _dtype(x.dtype), x.stride(0) if W.rows > 1 else W.cols,
+    _check(lib().qmv_quantize(ctypes.byref(W), x.data_ptr(), code, x.stride(0) if W.rows > 1 else W.cols,
                               _stream(stream, x)))
 
 

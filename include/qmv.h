@@ -238,6 +238,9 @@ int32_t qmv_create_weights(int32_t fmt, int64_t rows, int64_t cols,
  * Other Q4_K x bf16 calls with batch >= 2 run the matrix-core path (weights
  * read once for up to 16 activation rows, once per tile of 32, 64 or 128
  * rows above; exact products, fp32 sums, results independent of timing).
+ * MXFP4 x fp16 and bf16 with 5 or more rows (3 or more for cols > 4096) runs
+ * on the matrix cores too (exact products, fp32 sums, independent of timing,
+ * weights read once for 16 rows); fewer rows equal the batch-1 call.
  * Otherwise each activation row is a GEMV over the packed weights.  Q4_K,
  * Q5_K and Q6_K weights in QMV_LAYOUT_PLANES run the same arithmetic, in the
  * same order, as the canonical layout on every one of these paths, so
@@ -596,7 +599,8 @@ typedef struct qmv_mx4_args {
  * descriptor), QMV_ERR_SHAPE (columns differ, W->rows no multiple of experts or
  * of its halves, more rows than X without x_index, y_row below y's columns, y
  * overlaps W or X), QMV_ERR_ALIGN, QMV_ERR_UNSUPPORTED (dtype, epilogue, sizes
- * past the limits: 2^22 rows, 2^26 outputs of a matrix).  Enqueues only; no workspace; legal inside
+ * past the limits: 2^22 rows, 2^26 outputs and 2^32 bytes of codes of a
+ * matrix, 2^32 of X, 2^28 tiles).  Enqueues only; no workspace; legal inside
  * HIP stream capture. */
 int32_t qmv_mx4_gemm(const qmv_mx4_args* a, void* stream);
 

@@ -184,3 +184,55 @@ def test_two_streams_and_replays():
         for e, (a, b) in enumerate(((0, cut), (cut, cut), (cut, 50))):
             if b > a:
                 within(ys[0][a:b], *outputs(x[a:b], W.w[e * n:(e + 1) * n], False), torch.float32)
+
+
+def on_gpu(m, rows=None):
+    """64-bit values of an Mx's rows on the GPU."""
+    w = torch.from_numpy(m.w)
+    return (w if rows is None else w[rows]).to(DEV)
+
+
+# Shapes with more tiles than workgroups stay (each takes several in turn, the next one's first stages loaded ahead), of
+# one stage, of fewer than the ring's four, of parts of a stage, and of many; and with fewer tiles, for each kernel that
+# the launch chooses from.
+@pytest.mark.parametrize("m,n,k", [(4100, 9000, 32), (3000, 7000, 160), (5000, 4990, 384), (4096, 5120, 512), (3001, 6007, 1440),
+                                   (2500, 9000, 2048), (12, 20000, 96), (60, 20000, 256), (20, 9001, 1056), (100, 3584, 1568)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_tiles(m, n, k, swiglu):
+    say(f"mx4 gemm {m} x {n} x {k} swiglu {swiglu}")
+    n = n // 2 if swiglu else n
+    W, X = Mx(n * (2 if swiglu else 1), k, m + n, -6, -3), Mx(m, k, m + 1, -3, 1)
+    for dt in (("f32", "bf16") if m > 200 else list(TYPES)):
+        y = run(W, X, m, n, dt, swiglu)
+        x, w = on_gpu(X), on_gpu(W)
+        want, tol = x @ w.T, (x.abs() @ w.abs().T) * k * 2.0**-23
+        if swiglu:
+            (g, u), (dg, du) = want.chunk(2, -1), tol.chunk(2, -1)
+            s = g / (1 + torch.exp(-g))
+            want, tol = s * u, 1.1 * dg * (u.abs() + du) + s.abs() * du + 2.0**-20 * (s * u).abs()
+        f = torch.finfo(TYPES[dt])
+        tol = tol + f.eps / 2 * (want.abs() + tol) + f.smallest_normal * f.eps
+        assert bool(((y.double() - want).abs() <= tol).all())
+
+
+def test_many_tiles_of_experts():
+    """Enough ragged groups for several tiles to a workgroup, with indices outside and rows of no expert."""
+    experts, n, k, tokens, rows = 70, 700, 288, 900, 9000
+    W, X = Mx(experts * 2 * n, k, 1, -6, -3), Mx(tokens, k, 2, -3, 1)
+    r = np.random.default_rng(7)
+    cuts = np.sort(r.integers(20, rows - 30, experts - 1))
+    start = [20] + cuts.tolist() + [rows - 30]
+    idx = r.integers(-2, tokens + 2, rows)
+    y = run(W, X, rows, n, "f32", True, start, idx.tolist())
+    x = on_gpu(X)[torch.from_numpy(np.clip(idx, 0, tokens - 1)).to(DEV)]
+    x[torch.from_numpy((idx < 0) | (idx >= tokens)).to(DEV)] = 0
+    for e in range(experts):
+        a, b = start[e], start[e + 1]
+        w = on_gpu(W, slice(e * 2 * n, (e + 1) * 2 * n))
+        g, u = (x[a:b] @ w.T).chunk(2, -1)
+        mag = (x[a:b].abs() @ w.abs().T) * k * 2.0**-23
+        dg, du = mag.chunk(2, -1)
+        s = g / (1 + torch.exp(-g))
+        tol = 1.1 * dg * (u.abs() + du) + s.abs() * du + 2.0**-20 * (s * u).abs() + 1e-38
+        assert bool(((y[a:b].double() - s * u).abs() <= tol).all()), e
+    assert bool((y[:20] == 7.0).all()) and bool((y[-30:] == 7.0).all())

@@ -101,7 +101,10 @@ def test_mx4_gemm_refusals():
     a = _mx4()
     a.keep[1].nbytes += 1
     assert _gemm(a) == -5
-    # (2^22 rows of 2^31 outputs would be more tiles than a launch has)
+    # (too many outputs; more bytes of codes than 32 bits count)
+    assert _gemm(_mx4(W=_w((1 << 27) + 64, 64), y_row=(1 << 27) + 64, y=FAKE + (1 << 43))) == -6
+    assert _gemm(_mx4(W=_w(1 << 21, 8192), X=_w(10, 8192, at=FAKE + (1 << 42)), y_row=1 << 21, y=FAKE + (1 << 43))) == -6
+    assert _gemm(_mx4(W=_w(96, 8192), X=_w(1 << 21, 8192, at=FAKE + (1 << 42)), x_index=FAKE, y=FAKE + (1 << 43))) == -6
     assert _gemm(_mx4(W=_w((1 << 31) - 1, 32), X=_w(1 << 22, 32, at=FAKE + (1 << 42)), rows=1 << 22,
                       y_row=(1 << 31) - 1, y=FAKE + (1 << 43))) == -6
     a = _mx4(rows=0, y=None)
