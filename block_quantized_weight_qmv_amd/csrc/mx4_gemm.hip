@@ -503,12 +503,12 @@ mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
 #pragma unroll
       for (int s = 0; s < 3; ++s) copy_stage(next_from, s, (base + s) & 3);
       keep_scales();
+      __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
     }
     none = next_none;
     from = next_from;
     ahead_of = 0;
     wait_from = begun ? 2 : 0;
-    __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
 #pragma unroll
     for (int j = 0; j < TM; ++j) xf[0][j] = read_x(0, j), sb[j] = read_scale(0, BN + 16 * (wm * TM + j));
