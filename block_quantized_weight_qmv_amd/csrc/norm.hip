@@ -3,11 +3,16 @@
 // norm(x) = (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias, with
 // mean = 0 for RMS norms.
 //
-// Bound: HBM (each number is read and written once).  A row lives in the
-// registers of its threads between the sums, so that the block's norm, the
-// residual's sum and the next block's norm are one pass; sums are fp32, those
-// of a layer norm around the row's mean.  Rows of up to 2048 numbers belong to
-// one wave (no barrier, four rows to a workgroup), longer ones to a workgroup.
+// Bound: HBM (each number is read and written once); a few rows take a launch and
+// the latency of their loads.  A row lives in the registers of its threads between
+// the sums, so that the block's norm, the residual's sum and the next block's norm
+// are one pass; sums are fp32, those of a layer norm around the row's mean.  Rows of
+// up to 2048 numbers belong to one wave (no barrier, four rows to a workgroup),
+// longer ones to a workgroup.  A thread holds runs of eight numbers, loaded as 16
+// bytes whatever the row's alignment; rows that do not end with a whole run pay a
+// branch for each (bf16, both norms and the sum's store, 8 bytes a number: 16384
+// rows of 3584 90 us, 5.2 TB/s; of 3590 126 us, 326 when loaded number by number;
+// 65536 of 512 48 us, 5.5 TB/s).
 #include "launch.h"
 #include "mx4.h"
 
@@ -21,74 +26,74 @@ struct NormArgs {
   float eps, scale;
 };
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(_Float16 v) { return static_cast<float>(v); }
-__device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v.bits); }
-
-// Numbers at(k) of a row, k = 0 .. 8 VPT: with VEC eight consecutive ones for
-// each step of the row's threads (16-byte loads), else one (any alignment).
-template <int VPT, bool VEC>
+// Numbers at(k) of a row, k = 0 .. 8 VPT: eight consecutive ones for each step of
+// the row's threads.  WHOLE: the row is a number of whole eights.
+template <int VPT, bool WHOLE>
 struct RowMap {
   int t, threads, cols;
-  __device__ int at(int k) const { return VEC ? ((k >> 3) * threads + t) * 8 + (k & 7) : k * threads + t; }
+  __device__ int at(int k) const { return ((k >> 3) * threads + t) * 8 + (k & 7); }
   __device__ bool ok(int k) const { return at(k) < cols; }
 };
 
+// Sixteen bytes at any alignment of their elements.
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
 // Raw numbers of a row (zero past its end), converted later, so that the loads
 // of all the row's inputs are in flight together.
-template <typename T, int VPT, bool VEC>
+template <typename T, int VPT, bool WHOLE>
 struct RawRow {
   static constexpr int kPer = 8 * static_cast<int>(sizeof(T)) / 16;
-  uint4 raw[VEC ? VPT * kPer : 1];
-  T one[VEC ? 1 : 8 * VPT];
-  __device__ void load(const T* p, const RowMap<VPT, VEC>& m) {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          raw[j * kPer + i] = m.ok(8 * j) ? reinterpret_cast<const uint4*>(p + m.at(8 * j))[i] : make_uint4(0, 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8 * VPT; ++k) one[k] = m.ok(k) ? p[m.at(k)] : T{};
-    }
-  }
-  __device__ void get(float* v) const {
-    if constexpr (VEC) {
-      x_to_f32<8 * VPT>(raw, v, static_cast<const T*>(nullptr));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8 * VPT; ++k) v[k] = to_f32(one[k]);
-    }
-  }
-};
-
-template <int OUT, int VPT, bool VEC>
-__device__ __forceinline__ void store_row(void* p, const float* v, const RowMap<VPT, VEC>& m) {
-  if constexpr (VEC) {
+  uint4 raw[VPT * kPer];
+  __device__ void load(const T* p, const RowMap<VPT, WHOLE>& m) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (!m.ok(8 * j)) continue;
-      const float* w = v + 8 * j;
-      if constexpr (OUT == QMV_F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + m.at(8 * j));
-        o[0] = make_float4(w[0], w[1], w[2], w[3]);
-        o[1] = make_float4(w[4], w[5], w[6], w[7]);
-      } else {
-        auto two = [&](int k) { return OUT == QMV_F16 ? pack_f16(w[k], w[k + 1]) : pack_bf16(w[k], w[k + 1]); };
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + m.at(8 * j)) = make_uint4(two(0), two(2), two(4), two(6));
+      const T* q = p + m.at(8 * j);
+      const int left = m.cols - m.at(8 * j);
+      if (left >= 8) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const u32x4_a2 v = reinterpret_cast<const u32x4_a2*>(q)[i];
+          raw[j * kPer + i] = make_uint4(v.x, v.y, v.z, v.w);
+        }
+      } else if (WHOLE) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) raw[j * kPer + i] = make_uint4(0, 0, 0, 0);
+      } else {  // the row's last few, by one thread
+        T one[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) one[e] = e < left ? q[e] : T{};
+        __builtin_memcpy(&raw[j * kPer], one, sizeof(one));
       }
     }
-  } else {
+  }
+  __device__ void get(float* v) const { x_to_f32<8 * VPT>(raw, v, static_cast<const T*>(nullptr)); }
+};
+
+template <int OUT, int VPT, bool WHOLE>
+__device__ __forceinline__ void store_row(void* p, const float* v, const RowMap<VPT, WHOLE>& m) {
+  constexpr int kSize = OUT == QMV_F32 ? 4 : 2, kPer = 8 * kSize / 16;
 #pragma unroll
-    for (int k = 0; k < 8 * VPT; ++k) {
-      if (!m.ok(k)) continue;
-      if constexpr (OUT == QMV_F32)
-        static_cast<float*>(p)[m.at(k)] = v[k];
-      else if constexpr (OUT == QMV_F16)
-        static_cast<_Float16*>(p)[m.at(k)] = static_cast<_Float16>(v[k]);
-      else
-        static_cast<uint16_t*>(p)[m.at(k)] = static_cast<uint16_t>(pack_bf16(v[k], 0.f));
+  for (int j = 0; j < VPT; ++j) {
+    const float* w = v + 8 * j;
+    uint32_t d[4 * kPer];
+#pragma unroll
+    for (int i = 0; i < 4 * kPer; ++i)
+      d[i] = OUT == QMV_F32 ? __float_as_uint(w[i]) : OUT == QMV_F16 ? pack_f16(w[2 * i], w[2 * i + 1]) : pack_bf16(w[2 * i], w[2 * i + 1]);
+    uint8_t* o = static_cast<uint8_t*>(p) + static_cast<int64_t>(m.at(8 * j)) * kSize;
+    const int left = m.cols - m.at(8 * j);
+    if (left >= 8) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        reinterpret_cast<u32x4_a2*>(o)[i] = u32x4_a2{d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
+    } else if (!WHOLE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e >= left) continue;
+        if constexpr (OUT == QMV_F32)
+          reinterpret_cast<uint32_t*>(o)[e] = d[e];
+        else
+          reinterpret_cast<uint16_t*>(o)[e] = static_cast<uint16_t>(d[e / 2] >> (16 * (e & 1)));
+      }
     }
   }
 }
@@ -111,9 +116,9 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
 }
 
 // v = norm(v) of kind QMV_NORM_RMS or QMV_NORM_LAYER.
-template <typename W, int VPT, bool VEC, bool WAVE>
-__device__ __forceinline__ void norm_row(float* v, int kind, const RawRow<W, VPT, VEC>& w, const RawRow<W, VPT, VEC>& b,
-                                         bool has_w, bool has_b, const RowMap<VPT, VEC>& m, float eps, float* slot) {
+template <typename W, int VPT, bool WHOLE, bool WAVE>
+__device__ __forceinline__ void norm_row(float* v, int kind, const RawRow<W, VPT, WHOLE>& w, const RawRow<W, VPT, WHOLE>& b,
+                                         bool has_w, bool has_b, const RowMap<VPT, WHOLE>& m, float eps, float* slot) {
   constexpr int N = 8 * VPT;
   const float count = 1.0f / static_cast<float>(m.cols);
   if (kind == QMV_NORM_LAYER) {
@@ -143,17 +148,17 @@ __device__ __forceinline__ void norm_row(float* v, int kind, const RawRow<W, VPT
   }
 }
 
-template <typename T, typename W, int VPT, bool VEC, bool WAVE>
-__global__ void __launch_bounds__(WAVE ? 256 : 1024)
+template <typename T, typename W, int VPT, bool WHOLE, int MAXT, bool WAVE>
+__global__ void __launch_bounds__(MAXT)
 norm_kernel(const NormArgs a, int row0) {
   constexpr int N = 8 * VPT;
   __shared__ float slots[64];
-  const RowMap<VPT, VEC> m{WAVE ? static_cast<int>(threadIdx.x & 63) : static_cast<int>(threadIdx.x),
-                           WAVE ? 64 : static_cast<int>(blockDim.x), a.cols};
+  const RowMap<VPT, WHOLE> m{WAVE ? static_cast<int>(threadIdx.x & 63) : static_cast<int>(threadIdx.x),
+                                  WAVE ? 64 : static_cast<int>(blockDim.x), a.cols};
   const int64_t r = row0 + (WAVE ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x);
   if (WAVE && r >= a.rows) return;
-  typedef RawRow<T, VPT, VEC> Row;
-  typedef RawRow<W, VPT, VEC> Weights;
+  typedef RawRow<T, VPT, WHOLE> Row;
+  typedef RawRow<W, VPT, WHOLE> Weights;
   Row res, blk, gate;
   Weights pre_w, pre_b, post_w, post_b;
   res.load(static_cast<const T*>(a.residual) + r * a.residual_row, m);
@@ -169,7 +174,7 @@ norm_kernel(const NormArgs a, int row0) {
     float b[N];
     blk.get(b);
     if (a.post != QMV_NORM_NONE)
-      norm_row<W, VPT, VEC, WAVE>(b, a.post, post_w, post_b, a.post_w, a.post_b, m, a.eps, slots);
+      norm_row<W, VPT, WHOLE, WAVE>(b, a.post, post_w, post_b, a.post_w, a.post_b, m, a.eps, slots);
     if (a.gate) {
       float g[N];
       gate.get(g);
@@ -185,7 +190,7 @@ norm_kernel(const NormArgs a, int row0) {
   }
   if (!a.y) return;
   if (a.pre != QMV_NORM_NONE)
-    norm_row<W, VPT, VEC, WAVE>(s, a.pre, pre_w, pre_b, a.pre_w, a.pre_b, m, a.eps, slots + 32);
+    norm_row<W, VPT, WHOLE, WAVE>(s, a.pre, pre_w, pre_b, a.pre_w, a.pre_b, m, a.eps, slots + 32);
   if (a.y_dtype == QMV_F32)
     store_row<QMV_F32>(static_cast<float*>(a.y) + r * a.y_row, s, m);
   else if (a.y_dtype == QMV_F16)
@@ -194,39 +199,48 @@ norm_kernel(const NormArgs a, int row0) {
     store_row<QMV_BF16>(static_cast<uint16_t*>(a.y) + r * a.y_row, s, m);
 }
 
-template <typename T, typename W, int VPT, bool VEC>
+// WAVE: a wave to a row, four rows to a workgroup; else a workgroup of up to MAXT.
+template <typename T, typename W, int VPT, int MAXT, bool WAVE, bool WHOLE>
 static hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
-  const bool wave = a.cols <= 64 * 8 * VPT;
-  const int per = 8 * VPT, threads = wave ? 256 : ((a.cols + per - 1) / per + 63) / 64 * 64;
+  constexpr int per = 8 * VPT;
+  const int threads = WAVE ? 256 : ((a.cols + per - 1) / per + 63) / 64 * 64;
   // (a launch's work-items along x are counted in 32 bits)
   constexpr int most = 1 << 21;
-  for (int r = 0; r < a.rows; r += most) {
-    const int rows = a.rows - r < most ? a.rows - r : most;
-    if (wave)
-      hipLaunchKernelGGL((norm_kernel<T, W, VPT, VEC, true>), dim3((rows + 3) / 4), dim3(256), 0, s, a, r);
-    else
-      hipLaunchKernelGGL((norm_kernel<T, W, VPT, VEC, false>), dim3(rows), dim3(threads), 0, s, a, r);
+  for (int64_t r = 0; r < a.rows; r += most) {
+    const int rows = static_cast<int>(a.rows - r < most ? a.rows - r : most);
+    hipLaunchKernelGGL((norm_kernel<T, W, VPT, WHOLE, MAXT, WAVE>), dim3(WAVE ? (rows + 3) / 4 : rows), dim3(threads), 0, s,
+                       a, static_cast<int>(r));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-// Numbers to a thread: eight for rows that one wave holds so or that need no
-// more than 1024 threads so, else 32.
+// Numbers to a thread.  Eight for rows that one wave holds so, and for few longer
+// rows, whose latency counts; sixteen for many rows of a workgroup (16384 rows of
+// 3584 in bf16, both norms: 90 us, 108 with eight); else 32, whose workgroups of
+// more than 512 threads spill registers (1024 rows of 16384 36 us, of 32768 119).
+template <typename T, typename W, bool WHOLE>
+static hipError_t norm_typed(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 512) return norm_launch<T, W, 1, 256, true, WHOLE>(a, s);
+  if (a.cols <= 2048) return norm_launch<T, W, 4, 256, true, WHOLE>(a, s);
+  if (a.cols <= 8192 && a.rows < 1024) return norm_launch<T, W, 1, 1024, false, WHOLE>(a, s);
+  if (a.cols <= 8192) return norm_launch<T, W, 2, 512, false, WHOLE>(a, s);
+  if (a.cols <= 16384) return norm_launch<T, W, 4, 512, false, WHOLE>(a, s);
+  return norm_launch<T, W, 4, 1024, false, WHOLE>(a, s);
+}
+
 template <typename T, typename W>
-static hipError_t norm_typed(const NormArgs& a, bool vec, hipStream_t s) {
-  const bool wide = a.cols > 512 && (a.cols <= 2048 || a.cols > 8192);
-  if (vec) return wide ? norm_launch<T, W, 4, true>(a, s) : norm_launch<T, W, 1, true>(a, s);
-  return wide ? norm_launch<T, W, 4, false>(a, s) : norm_launch<T, W, 1, false>(a, s);
+static hipError_t norm_whole(const NormArgs& a, hipStream_t s) {
+  return a.cols % 8 ? norm_typed<T, W, false>(a, s) : norm_typed<T, W, true>(a, s);
 }
 
 template <typename T>
-static hipError_t norm_weights(const NormArgs& a, int w_dtype, bool vec, hipStream_t s) {
+static hipError_t norm_weights(const NormArgs& a, int w_dtype, hipStream_t s) {
   switch (w_dtype) {
-    case QMV_F32: return norm_typed<T, float>(a, vec, s);
-    case QMV_F16: return norm_typed<T, _Float16>(a, vec, s);
-    default: return norm_typed<T, bf16_t>(a, vec, s);
+    case QMV_F32: return norm_whole<T, float>(a, s);
+    case QMV_F16: return norm_whole<T, _Float16>(a, s);
+    default: return norm_whole<T, bf16_t>(a, s);
   }
 }
 
@@ -239,23 +253,10 @@ hipError_t norm(const qmv_norm_args& n, hipStream_t s) {
   a.sum_row = n.sum_row, a.y_row = n.y_row;
   a.rows = static_cast<int>(n.rows), a.cols = static_cast<int>(n.cols);
   a.pre = n.pre, a.post = n.post, a.y_dtype = n.y_dtype, a.eps = n.eps, a.scale = n.scale;
-  // 16-byte accesses where every row of everything starts on 16 bytes and ends
-  // with a whole eight
-  bool vec = n.cols % 8 == 0;
-  auto check = [&](const void* p, int64_t row, int size) {
-    if (p && ((reinterpret_cast<uintptr_t>(p) & 15) || (n.rows > 1 && row * size % 16))) vec = false;
-  };
-  const int xs = n.dtype == QMV_F32 ? 4 : 2;
-  check(n.residual, n.residual_row, xs);
-  check(n.block, n.block_row, xs);
-  check(n.gate, n.gate_row, xs);
-  check(n.sum, n.sum_row, xs);
-  check(n.y, n.y_row, n.y_dtype == QMV_F32 ? 4 : 2);
-  for (const void* p : {n.pre_weight, n.pre_bias, n.post_weight, n.post_bias}) check(p, 0, 0);
   switch (n.dtype) {
-    case QMV_F32: return norm_weights<float>(a, n.weight_dtype, vec, s);
-    case QMV_F16: return norm_weights<_Float16>(a, n.weight_dtype, vec, s);
-    default: return norm_weights<bf16_t>(a, n.weight_dtype, vec, s);
+    case QMV_F32: return norm_weights<float>(a, n.weight_dtype, s);
+    case QMV_F16: return norm_weights<_Float16>(a, n.weight_dtype, s);
+    default: return norm_weights<bf16_t>(a, n.weight_dtype, s);
   }
 }
 

@@ -607,7 +607,7 @@ int32_t qmv_mx4_gemm(const qmv_mx4_args* a, void* stream);
 enum { QMV_NORM_NONE = 0, QMV_NORM_RMS = 1, QMV_NORM_LAYER = 2 };
 
 /* Arguments of qmv_norm.  Row strides count elements; pointers are aligned by
- * their type (16-byte aligned rows of a multiple of 8 columns run fastest). */
+ * their type. */
 typedef struct qmv_norm_args {
   int32_t dtype;          /* residual, block, gate and sum                   */
   int32_t weight_dtype;   /* the weights and biases                          */
