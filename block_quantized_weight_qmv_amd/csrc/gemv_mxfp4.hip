@@ -18,7 +18,8 @@
 // and one v_dot2_f32_f16 for two weights against the activations as fp16 (fp16
 // as given, bf16 scaled per lane by 2^-e; exact, half_scale_exp).
 //
-// Bound: HBM at one and two rows (17/32 byte a weight).
+// Bound: HBM at one and two rows (17/32 byte a weight): 18944 x 3584 with one fp32
+// row takes 9.5 us (3.8 TB/s with the start and end of the launch).
 #include "gemv_skeleton.h"
 
 namespace qmv {

@@ -219,7 +219,8 @@ __device__ __forceinline__ uint2 scales8(const uint8_t* p, int b, int blocks) {
 // W-th piece of 256 columns (a whole line of every row) and add their sums in
 // LDS.  Fragments go from memory to the matrix instruction without LDS, D
 // pieces of a wave ahead: the weights' bytes bound it, and what is in flight
-// decides how near it comes.
+// decides how near it comes (16 rows against 2 x 18944 x 3584 with GLU 18.1 us,
+// 4.0 TB/s; 32 rows spread over 27 experts of 2 x 2560 x 3584 41.4 us, 6.3 TB/s).
 template <int NT, int MT, int W, int D, int OUT, bool GLU>
 __global__ void __launch_bounds__(64 * W)
 mx4_stream_kernel(const Mx4Launch a, int tiles_n) {
@@ -338,6 +339,12 @@ __device__ __forceinline__ int slot4(int piece, int r) { return piece ^ (0x78 >>
 // A workgroup stays for as many tiles as there are (grid = what the GPU holds):
 // the next tile's first stages, and its scales, are loaded while this one's
 // last stages are multiplied, and its results leave while the next one begins.
+//
+// Bound: the copies to LDS (a wave's instruction of 1 KB takes about 27 clocks,
+// four or eight a stage and wave) and what is done once a stage, beside the matrix
+// instructions, which alone would take half of the time: 4096 rows against
+// 18944 x 3584 take 162 us (3.4 PFLOP/s; random codes keep matrix instructions on
+// registers at 6.5 to 7.2), 32768 rows of 32 experts of 2 x 2560 x 2048 258 us (2.7).
 template <int WN, int WM, int TN, int TM, int OUT, bool GLU>
 __global__ void __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, 2)))
 mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
@@ -652,13 +659,13 @@ static hipError_t launch_stream(const Mx4Launch& a, hipStream_t s) {
 }
 
 // What a launch of tiles of 16 nt weight rows x 16 mt activation rows is expected
-// to take (us): `each` for every CU's share of them at 3584 columns, one tile's
-// own way at least.
-static double stream_cost(const Mx4Launch& a, bool glu, int nt, int mt, double each, double least) {
+// to take (us), at 3584 columns: `lone` where no CU has more than one, else `each`
+// for every one of the fullest CU's.
+static double stream_cost(const Mx4Launch& a, bool glu, int nt, int mt, double each, double lone) {
   const double tiles = tiles_n_of(a, glu, nt) * usual_tiles(a, 16 * mt);
   // (a launch's work-items along x are counted in 32 bits)
   if (tiles_n_of(a, glu, nt) * most_tiles(a, 16 * mt) >= 1 << 22) return 1e30;
-  return 2.5 + a.k / 3584.0 * std::max(least, each * tiles / 256);
+  return 2.5 + a.k / 3584.0 * (tiles <= 256 ? lone : each * std::ceil(tiles / 256));
 }
 
 template <int OUT, bool GLU>
@@ -666,12 +673,25 @@ static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
   // The kernel that is expected to end first.  The figures are measured ones at
   // 3584 columns: for a stream kernel, time a tile takes of a CU that has several,
   // and a lone tile's; for the tile kernels, time of one tile on each CU, and
-  // (128 x 128) of two.
+  // (128 x 128) of two.  All seven in this order, us (bf16 outputs, no GLU, weights
+  // beyond the caches), * the one chosen:
+  //   rows x outputs x columns
+  //     16 x  1024 x  3584    4.5*   5.4    8.1    6.0    6.9   15.4   28.1
+  //     16 x 18944 x  3584   13.9   13.1*  15.0   17.3   20.9   17.9   31.9
+  //     16 x  3584 x 18944   14.0*  18.6   32.3   21.3   26.1   66.2    122
+  //     64 x  3584 x  3584   10.2    8.3    8.4    6.9*   9.5   15.7   28.2
+  //     64 x 18944 x  3584   37.9   33.1   29.1   30.4   27.8   18.3*  31.4
+  //    256 x  3584 x  3584   28.0   23.1   22.4   23.2   17.8   16.1*  29.3
+  //    512 x 18944 x  3584    265    223    180    212    164   44.4   35.9*
+  //   1024 x  3584 x  3584    100   84.8   69.6   78.1   59.0   17.1*  29.9
+  //   4096 x 18944 x  3584   2072   1725   1380   1649   1256    240    186*
+  // (with GLU, 32 rows of 32 experts of 2560 outputs: 64.8, 49.0, 40.7*, 72.5, 83.9,
+  // 46.1, 70.9)
   const double small = tiles_n_of(a, GLU, 8) * usual_tiles(a, 128), large = tiles_n_of(a, GLU, 16) * usual_tiles(a, 256);
   const double rest = small - 512 * std::floor(small / 512);
-  const double cost[7] = {GLU ? 1e30 : stream_cost(a, GLU, 1, 1, 2.2, 2.0), stream_cost(a, GLU, 2, 1, 3.4, 2.7),
-                          stream_cost(a, GLU, 4, 1, 5.0, 5.0),            stream_cost(a, GLU, 2, 2, 5.8, 3.5),
-                          stream_cost(a, GLU, 2, 4, 9.2, 6.5),
+  const double cost[7] = {GLU ? 1e30 : stream_cost(a, GLU, 1, 1, 2.2, 2.1), stream_cost(a, GLU, 2, 1, 3.4, 2.8),
+                          stream_cost(a, GLU, 4, 1, 5.2, 5.7),            stream_cost(a, GLU, 2, 2, 5.8, 4.0),
+                          stream_cost(a, GLU, 2, 4, 8.6, 6.5),
                           2.5 + a.k / 3584.0 * (20 * std::floor(small / 512) + (rest == 0 ? 0 : rest <= 256 ? 13.3 : 20)),
                           2.5 + a.k / 3584.0 * 27 * std::max(1.0, large / 256)};
   switch (std::min_element(cost, cost + 7) - cost) {
