@@ -220,7 +220,7 @@ __device__ __forceinline__ uint2 scales8(const uint8_t* p, int b, int blocks) {
 // LDS.  Fragments go from memory to the matrix instruction without LDS, D
 // pieces of a wave ahead: the weights' bytes bound it, and what is in flight
 // decides how near it comes (16 rows against 2 x 18944 x 3584 with GLU 18.1 us,
-// 4.0 TB/s; 32 rows spread over 27 experts of 2 x 2560 x 3584 41.4 us, 6.3 TB/s).
+// 4.0 TB/s; 32 rows of 18 experts of 2 x 2560 x 3584 41.4 us, 4.2 TB/s).
 template <int NT, int MT, int W, int D, int OUT, bool GLU>
 __global__ void __launch_bounds__(64 * W)
 mx4_stream_kernel(const Mx4Launch a, int tiles_n) {
@@ -341,10 +341,11 @@ __device__ __forceinline__ int slot4(int piece, int r) { return piece ^ (0x78 >>
 // last stages are multiplied, and its results leave while the next one begins.
 //
 // Bound: the copies to LDS (a wave's instruction of 1 KB takes about 27 clocks,
-// four or eight a stage and wave) and what is done once a stage, beside the matrix
-// instructions, which alone would take half of the time: 4096 rows against
-// 18944 x 3584 take 162 us (3.4 PFLOP/s; random codes keep matrix instructions on
-// registers at 6.5 to 7.2), 32768 rows of 32 experts of 2 x 2560 x 2048 258 us (2.7).
+// four a stage and wave) and what is done once a stage, beside the matrix
+// instructions: their pipes are busy 37 % of the clocks, and waves wait for a third
+// of theirs.  4096 rows against 18944 x 3584 take 162 us (3.4 PFLOP/s; with random
+// codes and operands in registers alone 6.5 to 7.2), 32768 rows of 27 experts of
+// 2 x 2560 x 2048 258 us (2.7).
 template <int WN, int WM, int TN, int TM, int OUT, bool GLU>
 __global__ void __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2, 2)))
 mx4_tile_kernel(const Mx4Launch a, int tiles_n) {
@@ -685,8 +686,8 @@ static hipError_t launch(const Mx4Launch& a, hipStream_t s) {
   //    512 x 18944 x  3584    265    223    180    212    164   44.4   35.9*
   //   1024 x  3584 x  3584    100   84.8   69.6   78.1   59.0   17.1*  29.9
   //   4096 x 18944 x  3584   2072   1725   1380   1649   1256    240    186*
-  // (with GLU, 32 rows of 32 experts of 2560 outputs: 64.8, 49.0, 40.7*, 72.5, 83.9,
-  // 46.1, 70.9)
+  // (with GLU, 32 rows of 18 of 32 experts of 2560 outputs: 64.8, 49.0, 40.7*, 72.5,
+  // 83.9, 46.1, 70.9)
   const double small = tiles_n_of(a, GLU, 8) * usual_tiles(a, 128), large = tiles_n_of(a, GLU, 16) * usual_tiles(a, 256);
   const double rest = small - 512 * std::floor(small / 512);
   const double cost[7] = {GLU ? 1e30 : stream_cost(a, GLU, 1, 1, 2.2, 2.1), stream_cost(a, GLU, 2, 1, 3.4, 2.8),

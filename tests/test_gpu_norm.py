@@ -165,3 +165,14 @@ def test_many_rows_and_streams():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("cols", [2049, 2056, 5003, 8191, 8192])
+def test_many_long_rows(cols, dt):
+    """Sixteen numbers to a thread, of rows that end inside a run of eight and of rows that do not."""
+    say(f"norm 1030x{cols} {dt}")
+    t = data(1030, cols, dt, cols)
+    check(t["residual"], torch.empty(1030, cols, dtype=TYPES["bf16"], device=DEV), pre="rms", post="layer",
+          pre_weight=t["pre_weight"], post_weight=t["post_weight"], post_bias=t["post_bias"], block=t["block"],
+          gate=t["rows"], sum_out=torch.empty_like(t["residual"]))
