@@ -191,3 +191,11 @@ def test_norm_binding():
         _expect(status, create, **k)
     with pytest.raises(qmv.QmvError):
         qmv.qmv_norm(create(), 0)  # neither sum nor y
+
+
+def test_gemm_sizes_past_32_bits():
+    """Rows of X and columns that would be others when cut to 32 bits."""
+    far = FAKE + (1 << 43)
+    assert _gemm(_mx4(W=_w(96, 32), X=_w((1 << 32) + 5, 32, at=FAKE + (1 << 42)), x_index=FAKE, y=far)) == -6
+    assert _gemm(_mx4(W=_w(96, (1 << 32) + 32), X=_w(10, (1 << 32) + 32, at=FAKE + (1 << 42)), x_index=FAKE, y=far)) == -6
+    assert _gemm(_mx4(W=_w(2, 1 << 31), X=_w(2, 1 << 31, at=FAKE + (1 << 42)), rows=2, y=far)) == -6
