@@ -95,7 +95,8 @@ struct Mxfp4Policy {
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = max(top, max((word(i) << 16) & 0x7FFFFFFFu, word(i) & 0x7FFF0000u));
         const float mx[1] = {__uint_as_float(top)};
-        s.e = half_scale_exp<XT, 1>(mx);
+        // (beside an infinity finite numbers must not become one: the largest power)
+        s.e = mx[0] == __builtin_inff() ? 103 : half_scale_exp<XT, 1>(mx);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const uint32_t w = word(i);

@@ -15,8 +15,8 @@
 // columns to a wave, the sums joined in LDS.
 //
 // Bound: few loads in flight and many a byte (an activation row of 16 bits is four
-// times a weight row): 3 fp16 rows against 3584 x 18944 take 17.6 us (22.3 in the
-// GEMV's passes of two rows), 2.1 TB/s of weights; 16 rows 30 us (against 96).
+// times a weight row): 3 fp16 rows against 3584 x 18944 take 19.1 us (22.3 in the
+// GEMV's passes of two rows), 1.9 TB/s of weights; 16 rows 30 us (against 96).
 #include "launch.h"
 #include "mx4.h"
 
@@ -36,6 +36,13 @@ __device__ __forceinline__ bf16x8_t weights8(uint32_t q, float scale) {
   return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+// v without its first bits; of an infinity that infinity again, and of a NaN NaN
+// (fp16 ends at 65504, which changes no finite number here; 3 rows as above take
+// 17.6 us without it, infinities then being NaN)
+__device__ __forceinline__ float rest(float v, uint32_t first) {
+  return v - __builtin_amdgcn_fmed3f(__uint_as_float(first), -65504.f, 65504.f);
+}
+
 // Eight fp16 numbers as hi + lo, two bf16 numbers each: the first eight bits,
 // and the rest.
 __device__ __forceinline__ void halves8(const uint4& raw, bf16x8_t& hi, bf16x8_t& lo) {
@@ -46,7 +53,7 @@ __device__ __forceinline__ void halves8(const uint4& raw, bf16x8_t& hi, bf16x8_t
     const float a = f16_to_f32(w[i] & 0xFFFFu), b = f16_to_f32(w[i] >> 16);
     const uint32_t ua = __float_as_uint(a) & 0xFFFF0000u, ub = __float_as_uint(b) & 0xFFFF0000u;
     h[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302);
-    l[i] = __builtin_amdgcn_perm(__float_as_uint(b - __uint_as_float(ub)), __float_as_uint(a - __uint_as_float(ua)), 0x07060302);
+    l[i] = __builtin_amdgcn_perm(__float_as_uint(rest(b, ub)), __float_as_uint(rest(a, ua)), 0x07060302);
   }
   hi = __builtin_bit_cast(bf16x8_t, make_uint4(h[0], h[1], h[2], h[3]));
   lo = __builtin_bit_cast(bf16x8_t, make_uint4(l[0], l[1], l[2], l[3]));

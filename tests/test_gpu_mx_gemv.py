@@ -127,3 +127,24 @@ def test_fp16_rows_of_every_size_on_the_matrix_cores():
     one = torch.eye(16, 256, dtype=torch.float16, device=DEV) * 3.140625  # products stand alone: exact
     m = Mx(70, 256, 6)
     assert np.array_equal(gemv(m, one, "f16").cpu().double().numpy(), 3.140625 * m.w[:, :16].T)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("cols", [256, 4128])
+def test_infinities_and_nan_of_activations(cols, dt):
+    """An infinite activation makes its row's outputs infinite (NaN where the weight is zero), a NaN its row NaN."""
+    m = Mx(40, cols, 4)
+    column = m.w[:, 100]
+    assert (column == 0).any() and (column > 0).any() and (column < 0).any()
+    for batch in (1, 6, 18):
+        say(f"gemv infinities 40x{cols} {dt} batch {batch}")
+        x = x_of(batch, cols, dt, 6)
+        x[0, 100] = float("inf")
+        if batch > 1:
+            x[2, 100], x[5, 100] = float("-inf"), float("nan")
+        y = gemv(m, x, dt).cpu().double().numpy()
+        with np.errstate(invalid="ignore"):
+            for row, v in ((0, np.inf), (2, -np.inf))[:batch]:
+                np.testing.assert_array_equal(y[row], v * column)
+        if batch > 1:
+            assert np.isnan(y[5]).all() and np.isfinite(y[[1, 3, 4]]).all()
